@@ -1,0 +1,566 @@
+// Products of grouped rows with the packed weights of their experts, for
+// few rows per expert, and the weighted sum of a token's experts.
+//
+//   Y[p][n] = sum_k X[r(p)][k] w_e[n][k],  e = group of position p
+//
+// What bounds it: a decode step reads the packed weights of every expert
+// that some row takes, once, and little else; so the kernel is built to
+// stream codes, and the decoding of a weight is kept to a few integer
+// operations on lanes that the loads leave idle.
+//
+// Tile: 16 rows of one expert times 64 of its output columns, by a
+// workgroup of four waves that each take a quarter of K (their fp32 sums
+// are added in wave order through LDS). One v_mfma_f32_16x16x32 covers 16
+// rows, 16 columns and the 32 weights of one scale group, so the products
+// are with the bare code levels and the group's scale multiplies the fp32
+// sum: no weight is rounded to 16 bits, and the scaling costs four
+// multiply-adds a lane where scaling the weights would cost eight.
+//   2-bit: the levels +-1.52, +-0.45 enter as +-152, +-45 (exact in fp16
+//     and bf16), the sum is divided by 100 at the end; Z times the row sums
+//     of x, which come from the same A operand against a constant 100.
+//   INT4: u - 8 is exact. NF4: a level is two 16-bit numbers, the nearest
+//     and the rest, two products.
+// A code byte becomes 16-bit levels by one LDS table read. Lane l reads
+// replica l % 16 of the table, so no two of 16 lanes meet in a bank.
+//
+// A lane loads 64 consecutive codes of one column (16 bytes of 2-bit, 32 of
+// 4-bit codes); the matrix instruction wants eight per lane of 32
+// consecutive ones. A 4 x 4 transposition of dwords over the four lane
+// groups (two half-wave and two row swaps) turns one into the other.
+#include "op16.h"
+#include "row_groups.h"
+
+namespace qw {
+namespace {
+
+constexpr int kRows = 16;
+constexpr int kCols = 64;
+constexpr int kSub = kCols / 16;  // 16-column blocks of a tile
+constexpr int kWaves = 4;
+constexpr int kThreads = 64 * kWaves;
+constexpr int kChunk = 256;       // weights of one column in one set of loads
+
+struct ExpertArgs {
+  const uint16_t *X;        // [x_rows][K]
+  const uint8_t *codes;
+  const uint8_t *scales;
+  const int32_t *idx;       // 2-bit anchors [E][n_out]
+  const uint32_t *mask;     // 2-bit anchors [E][K/32]
+  const uint16_t *wo;       // anchors [E][N][n_out_pad], fp16
+  const int32_t *offsets, *rows;
+  void *Y;
+  int x_rows, x_div;
+  int G, n;                 // groups, positions
+  int N, K, out_n;          // weight rows, weight columns, columns of Y
+  int n_out, n_out_pad;
+  int col_tiles;
+  int swiglu, by_slot;      // by_slot: Y row rows[p] in place of p
+  int y_dtype;
+  float nf4[16];
+};
+
+__device__ inline __amdgpu_buffer_rsrc_t rsrc(const void *p, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), (short)0, (int)bytes, 0x00020000);
+}
+constexpr uint32_t kOob = 0x80000000u;  // an offset past every buffer's end (reads 0)
+
+__device__ inline void swap32(uint32_t &a, uint32_t &b) {
+  const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+  a = r[0];
+  b = r[1];
+}
+__device__ inline void swap16(uint32_t &a, uint32_t &b) {
+  const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+  a = r[0];
+  b = r[1];
+}
+// d[i] of lane group g (lanes 16g..16g+15) <-> d[g] of lane group i
+__device__ inline void transpose4(uint32_t (&d)[4]) {
+  swap32(d[0], d[2]);
+  swap32(d[1], d[3]);
+  swap16(d[0], d[1]);
+  swap16(d[2], d[3]);
+}
+// w of lane group i to all four lane groups, as out[i]
+__device__ inline void gather4(uint32_t w, uint32_t (&out)[4]) {
+  uint32_t a = w, b = w;
+  swap32(a, b);  // a: groups 0 1 0 1, b: groups 2 3 2 3
+  out[0] = out[1] = a;
+  out[2] = out[3] = b;
+  swap16(out[0], out[1]);
+  swap16(out[2], out[3]);
+}
+
+// Level table: entry of code byte v, replica r. 2-bit: four levels (8
+// bytes), INT4: two (4 bytes, two replicas side by side), NF4: the nearest
+// two and the rests of both (8 bytes).
+constexpr int kEntry = 128;  // bytes of one byte's replicas
+template <int FMT, int DT>
+__device__ inline void fill_table(char *tab, const ExpertArgs &a) {
+  for (int i = threadIdx.x; i < 256 * 8; i += kThreads) {
+    const int v = i >> 3;
+    u32x2 w;
+    if (FMT == QW_FMT_2BIT_G32) {
+      uint32_t l[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const int q = (v >> (2 * t)) & 3;
+        l[t] = Op<DT>::bits(q == 0 ? -152.0f : q == 1 ? -45.0f : q == 2 ? 45.0f : 152.0f);
+      }
+      w = u32x2{l[0] | (l[1] << 16), l[2] | (l[3] << 16)};
+    } else if (FMT == QW_FMT_INT4_G32) {
+      const uint32_t p = Op<DT>::bits((float)((v & 15) - 8)) | (Op<DT>::bits((float)((v >> 4) - 8)) << 16);
+      w = u32x2{p, p};
+    } else {
+      const float lo = a.nf4[v & 15], hi = a.nf4[v >> 4];
+      const uint32_t lo16 = Op<DT>::bits(lo), hi16 = Op<DT>::bits(hi);
+      w = u32x2{lo16 | (hi16 << 16),
+                Op<DT>::bits(lo - Op<DT>::value(lo16)) | (Op<DT>::bits(hi - Op<DT>::value(hi16)) << 16)};
+    }
+    *reinterpret_cast<u32x4 *>(tab + v * kEntry + (i & 7) * 16) = u32x4{w[0], w[1], w[0], w[1]};
+  }
+}
+
+// The tile's gathered loads of one chunk: codes and scale words of the
+// lane's 64 weights in each of the four 16-column blocks.
+template <int FMT>
+struct Chunk {
+  static constexpr int kCodes = FMT == QW_FMT_2BIT_G32 ? 4 : 8;   // dwords
+  static constexpr int kScales = FMT == QW_FMT_2BIT_G32 ? 2 : 1;  // dwords
+  uint32_t c[kSub][kCodes];
+  uint32_t s[kSub][kScales];
+};
+
+template <int FMT, int DT, bool ANCH>
+__global__ __launch_bounds__(kThreads) void experts_kernel(ExpertArgs a) {
+  using O = Op<DT>;
+  __shared__ __attribute__((aligned(16))) char tab[256 * kEntry];
+  __shared__ __attribute__((aligned(16))) float part[kWaves][kRows][kCols + 4];
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int ln = lane & 15, lg = lane >> 4;
+  const int tile = blockIdx.x / a.col_tiles, ct = blockIdx.x % a.col_tiles;
+  const RowTile rt = find_row_tile(a.offsets, a.G, a.n, kRows, tile);
+  if (rt.cnt == 0) return;
+  const int e = rt.g, K = a.K;
+
+  fill_table<FMT, DT>(tab, a);
+
+  // this lane's row of A: rows past the tile's end repeat its first row
+  // (their products are not stored)
+  const int p = rt.p0 + (ln < rt.cnt ? ln : 0);
+  int xr = a.x_div ? a.rows[p] / a.x_div : p;
+  if ((uint32_t)xr >= (uint32_t)a.x_rows) xr = 0;
+  const uint16_t *const xp = a.X + (size_t)xr * K;
+
+  // columns: gated tiles take 32 gate columns and the same 32 up columns
+  const int half_cols = a.swiglu ? kCols / 2 : kCols;
+  const int c0 = ct * half_cols;
+  uint32_t co[kSub], so[kSub];
+  constexpr int kCodeDiv = FMT == QW_FMT_2BIT_G32 ? 4 : 2;     // weights per code byte
+  constexpr int kScaleDiv = FMT == QW_FMT_2BIT_G32 ? 8 : 16;   // weights per scale byte
+  const size_t cb = (size_t)a.N * (K / kCodeDiv), sb = (size_t)a.N * (K / kScaleDiv);
+  const auto rc = rsrc(a.codes + (size_t)e * cb, (uint32_t)cb);
+  const auto rs = rsrc(a.scales + (size_t)e * sb, (uint32_t)sb);
+  int wn[kSub];
+#pragma unroll
+  for (int j = 0; j < kSub; ++j) {
+    int n = c0 + j * 16 + ln;
+    bool in = n < a.out_n;
+    if (a.swiglu) {
+      const int h = c0 + (j & 1) * 16 + ln;
+      in = h < a.out_n;
+      n = h + (j >> 1) * a.out_n;
+    }
+    wn[j] = in ? n : -1;
+    co[j] = in ? (uint32_t)n * (uint32_t)(K / kCodeDiv) : kOob;
+    so[j] = in ? (uint32_t)n * (uint32_t)(K / kScaleDiv) : kOob;
+  }
+
+  // this wave's chunks
+  const int chunks = (K + kChunk - 1) / kChunk;
+  const int per = (chunks + kWaves - 1) / kWaves;
+  const int ch0 = min(wv * per, chunks), ch1 = min(ch0 + per, chunks);
+
+  using CH = Chunk<FMT>;
+  auto load = [&](int ch, CH &d) {
+    const int k = ch * kChunk + lg * 64;
+    const bool in = k < K;
+#pragma unroll
+    for (int j = 0; j < kSub; ++j) {
+      const uint32_t oc = in && wn[j] >= 0 ? co[j] + (uint32_t)k / kCodeDiv : kOob;
+      const uint32_t os = in && wn[j] >= 0 ? so[j] + (uint32_t)k / kScaleDiv : kOob;
+#pragma unroll
+      for (int i = 0; i < CH::kCodes; i += 4) {
+        const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(rc, (int)(oc == kOob ? kOob : oc + 4 * i), 0, 0);
+        d.c[j][i] = v[0]; d.c[j][i + 1] = v[1]; d.c[j][i + 2] = v[2]; d.c[j][i + 3] = v[3];
+      }
+      if (CH::kScales == 2) {
+        const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(rs, (int)os, 0, 0);
+        d.s[j][0] = v[0];
+        d.s[j][CH::kScales - 1] = v[1];
+      } else {
+        d.s[j][0] = __builtin_amdgcn_raw_buffer_load_b32(rs, (int)os, 0, 0);
+      }
+    }
+  };
+
+  f32x4 acc[kSub];
+#pragma unroll
+  for (int j = 0; j < kSub; ++j) acc[j] = f32x4{0, 0, 0, 0};
+  const f32x4 zero = {0, 0, 0, 0};
+  const uint32_t rep = (uint32_t)(lane & 15) * 8u;
+  auto entry = [&](uint32_t byte) { return tab + ((byte << 7) | rep); };
+
+  // products of the eight 32-weight steps of a chunk
+  auto multiply = [&](int ch, CH &d) {
+    const int k0 = ch * kChunk;
+    const int steps = min(8, (K - k0) / 32);
+#pragma unroll
+    for (int j = 0; j < kSub; ++j) {
+      if (FMT == QW_FMT_2BIT_G32) {
+        // halves h0..h7 of the lane's 64 codes: dword g gets (h_g, h_4+g),
+        // so lane group g ends up with its 8 codes of steps 2s and 2s + 1
+        const uint32_t d0 = d.c[j][0], d1 = d.c[j][1], d2 = d.c[j][2], d3 = d.c[j][3];
+        d.c[j][0] = __builtin_amdgcn_perm(d2, d0, 0x05040100u);
+        d.c[j][1] = __builtin_amdgcn_perm(d2, d0, 0x07060302u);
+        d.c[j][2] = __builtin_amdgcn_perm(d3, d1, 0x05040100u);
+        d.c[j][3] = __builtin_amdgcn_perm(d3, d1, 0x07060302u);
+      }
+#pragma unroll
+      for (int i = 0; i < CH::kCodes; i += 4)
+        transpose4(reinterpret_cast<uint32_t(&)[4]>(d.c[j][i]));
+    }
+    uint32_t sc[kSub][CH::kScales][4];
+#pragma unroll
+    for (int j = 0; j < kSub; ++j)
+#pragma unroll
+      for (int i = 0; i < CH::kScales; ++i) gather4(d.s[j][i], sc[j][i]);
+
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+      if (t < steps) {
+        u32x4 A = *reinterpret_cast<const u32x4 *>(xp + k0 + t * 32 + lg * 8);
+        const int src = t >> 1, h = t & 1;  // source lane group and half of its run
+        f32x4 xs = zero;
+        if (FMT == QW_FMT_2BIT_G32) {
+          if (ANCH) {
+            const uint32_t m = a.mask[(size_t)e * (K / 32) + (k0 / 32 + t)] >> (8 * lg);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const uint32_t drop = ((m >> (2 * q)) & 1 ? 0xFFFFu : 0u) | ((m >> (2 * q + 1)) & 1 ? 0xFFFF0000u : 0u);
+              A[q] &= ~drop;
+            }
+          }
+          const uint32_t hundred = Op<DT>::bits(100.0f) * 0x10001u;
+          xs = O::mma(A, u32x4{hundred, hundred, hundred, hundred}, zero);
+        }
+#pragma unroll
+        for (int j = 0; j < kSub; ++j) {
+          u32x4 B, B2;
+          if (FMT == QW_FMT_2BIT_G32) {
+            const uint32_t c = d.c[j][src] >> (16 * h);
+            const u32x2 lo = *reinterpret_cast<const u32x2 *>(entry(c & 0xFFu));
+            const u32x2 hi = *reinterpret_cast<const u32x2 *>(entry((c >> 8) & 0xFFu));
+            B = u32x4{lo[0], lo[1], hi[0], hi[1]};
+          } else {
+            const uint32_t c = d.c[j][(4 * h + src) % CH::kCodes];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const char *en = entry((c >> (8 * q)) & 0xFFu);
+              if (FMT == QW_FMT_INT4_G32) {
+                B[q] = *reinterpret_cast<const uint32_t *>(en);
+              } else {
+                const u32x2 w = *reinterpret_cast<const u32x2 *>(en);
+                B[q] = w[0];
+                B2[q] = w[1];
+              }
+            }
+          }
+          f32x4 D = O::mma(A, B, zero);
+          if (FMT == QW_FMT_NF4_B64) {
+            D = O::mma(A, B2, D);
+            const float am = __builtin_bit_cast(float, sc[j][0][src]);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[j][r] = __builtin_fmaf(am, D[r], acc[j][r]);
+          } else if (FMT == QW_FMT_INT4_G32) {
+            const float s = f16_bits_to_f32((uint16_t)(sc[j][0][src] >> (16 * h)));
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[j][r] = __builtin_fmaf(s, D[r], acc[j][r]);
+          } else {
+            const uint32_t w = sc[j][h % CH::kScales][src];
+            const float S = f16_bits_to_f32((uint16_t)w), Z = f16_bits_to_f32((uint16_t)(w >> 16));
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[j][r] = __builtin_fmaf(S, D[r], __builtin_fmaf(Z, xs[r], acc[j][r]));
+          }
+        }
+      }
+    }
+  };
+
+  CH buf[2];
+  if (ch0 < ch1) load(ch0, buf[0]);
+  __syncthreads();  // the level table
+  for (int ch = ch0; ch < ch1; ch += 2) {
+    if (ch + 1 < ch1) load(ch + 1, buf[1]);
+    multiply(ch, buf[0]);
+    if (ch + 1 < ch1) {
+      if (ch + 2 < ch1) load(ch + 2, buf[0]);
+      multiply(ch + 1, buf[1]);
+    }
+  }
+  if (FMT == QW_FMT_2BIT_G32) {
+#pragma unroll
+    for (int j = 0; j < kSub; ++j) acc[j] *= 0.01f;
+  }
+
+  if (ANCH) {
+    // the anchor channels: 32 of them a step, the waves in turn. bf16
+    // operands take the fp16 anchor as two parts.
+    for (int o0 = wv * 32; o0 < a.n_out; o0 += kWaves * 32) {
+      const int o = o0 + lg * 8;
+      u32x4 A = {0, 0, 0, 0};
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        if (o + q < a.n_out) {
+          int k = o + q;
+          if (FMT == QW_FMT_2BIT_G32) {
+            k = a.idx[(size_t)e * a.n_out + o + q];
+            if ((uint32_t)k >= (uint32_t)K) k = 0;
+          }
+          A[q >> 1] |= (uint32_t)xp[k] << (16 * (q & 1));
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kSub; ++j) {
+        u32x4 B = {0, 0, 0, 0}, B2 = {0, 0, 0, 0};
+        if (wn[j] >= 0 && o < a.n_out_pad) {
+          B = *reinterpret_cast<const u32x4 *>(a.wo + ((size_t)e * a.N + wn[j]) * a.n_out_pad + o);
+          if (DT == QW_DT_BF16) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const float lo = f16_bits_to_f32((uint16_t)B[q]), hi = f16_bits_to_f32((uint16_t)(B[q] >> 16));
+              const uint32_t lo16 = O::bits(lo), hi16 = O::bits(hi);
+              B[q] = lo16 | (hi16 << 16);
+              B2[q] = O::bits(lo - O::value(lo16)) | (O::bits(hi - O::value(hi16)) << 16);
+            }
+          }
+        }
+        acc[j] = O::mma(A, B, acc[j]);
+        if (DT == QW_DT_BF16) acc[j] = O::mma(A, B2, acc[j]);
+      }
+    }
+  }
+
+  // ---- the four waves' sums, then one rounding ----
+#pragma unroll
+  for (int j = 0; j < kSub; ++j)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) part[wv][lg * 4 + r][j * 16 + ln] = acc[j][r];
+  __syncthreads();
+  const int row = tid >> 4;
+  if (row >= rt.cnt) return;
+  int yr = rt.p0 + row;
+  if (a.by_slot) {
+    yr = a.rows[yr];
+    if ((uint32_t)yr >= (uint32_t)a.n) return;
+  } else if (a.x_div && (uint32_t)(a.rows[yr] / a.x_div) >= (uint32_t)a.x_rows) {
+    return;
+  }
+  auto total = [&](int c) {
+    return *reinterpret_cast<const f32x4 *>(&part[0][row][c]) + *reinterpret_cast<const f32x4 *>(&part[1][row][c]) +
+           *reinterpret_cast<const f32x4 *>(&part[2][row][c]) + *reinterpret_cast<const f32x4 *>(&part[3][row][c]);
+  };
+  const int c = (tid & 15) * 4;
+  if (c >= half_cols) return;
+  f32x4 v = total(c);
+  if (a.swiglu) {
+    const f32x4 u = total(c + kCols / 2);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) v[q] = v[q] / (1.0f + expf(-v[q])) * u[q];
+  }
+  const int n = c0 + c;
+  const size_t o = (size_t)yr * a.out_n + n;
+  if (n + 4 <= a.out_n && a.out_n % 4 == 0) {
+    if (a.y_dtype == QW_DT_F32)
+      *reinterpret_cast<f32x4 *>(reinterpret_cast<float *>(a.Y) + o) = v;
+    else
+      *reinterpret_cast<u32x2 *>(reinterpret_cast<uint16_t *>(a.Y) + o) =
+          u32x2{out_bits(v[0], a.y_dtype) | (out_bits(v[1], a.y_dtype) << 16),
+                out_bits(v[2], a.y_dtype) | (out_bits(v[3], a.y_dtype) << 16)};
+  } else {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (n + q >= a.out_n) continue;
+      if (a.y_dtype == QW_DT_F32)
+        reinterpret_cast<float *>(a.Y)[o + q] = v[q];
+      else
+        reinterpret_cast<uint16_t *>(a.Y)[o + q] = (uint16_t)out_bits(v[q], a.y_dtype);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// out[t][n] = sum_j weights[t][j] P[t * k + j][n] over the slots that are in
+// a group: one read of the fp32 products, bound by memory. A thread takes
+// four columns of one token.
+struct CombineArgs {
+  const float *P;  // [T * k][N]
+  const int32_t *ids;
+  const float *weights;
+  void *out;
+  int T, k, N, E, dtype;
+  int col_blocks;
+};
+
+__global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) {
+  const int t = blockIdx.x / a.col_blocks;
+  const int n = ((int)(blockIdx.x % a.col_blocks) * 256 + (int)threadIdx.x) * 4;
+  if (n >= a.N) return;
+  const bool vec = a.N % 4 == 0;
+  f32x4 s = {0, 0, 0, 0};
+  for (int j = 0; j < a.k; ++j) {
+    const size_t slot = (size_t)t * a.k + j;
+    if ((uint32_t)a.ids[slot] >= (uint32_t)a.E) continue;  // wave-uniform
+    const float w = a.weights[slot];
+    const float *p = a.P + slot * a.N + n;
+    if (vec) {
+      const f32x4 v = *reinterpret_cast<const f32x4 *>(p);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) s[q] = __builtin_fmaf(w, v[q], s[q]);
+    } else {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (n + q < a.N) s[q] = __builtin_fmaf(w, p[q], s[q]);
+    }
+  }
+  const size_t o = (size_t)t * a.N + n;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    if (n + q >= a.N) continue;
+    if (a.dtype == QW_DT_F32)
+      reinterpret_cast<float *>(a.out)[o + q] = s[q];
+    else
+      reinterpret_cast<uint16_t *>(a.out)[o + q] = (uint16_t)out_bits(s[q], a.dtype);
+  }
+}
+
+template <int FMT, int DT, bool ANCH>
+qw_status launch_one(const ExpertArgs &a, hipStream_t s) {
+  const long long grid = most_row_tiles(a.n, a.G, kRows) * a.col_tiles;
+  if (grid >= (1ll << 31)) return QW_ERR_UNSUPPORTED;
+  QW_HIP_TRY(launch(experts_kernel<FMT, DT, ANCH>, (unsigned)grid, kThreads, 0, s, a));
+  return QW_OK;
+}
+
+template <int FMT, int DT>
+qw_status launch_anch(const ExpertArgs &a, hipStream_t s) {
+  if constexpr (FMT != QW_FMT_NF4_B64)
+    if (a.n_out > 0) return launch_one<FMT, DT, true>(a, s);
+  return launch_one<FMT, DT, false>(a, s);
+}
+
+template <int DT>
+qw_status launch_fmt(int fmt, const ExpertArgs &a, hipStream_t s) {
+  if (fmt == QW_FMT_2BIT_G32) return launch_anch<QW_FMT_2BIT_G32, DT>(a, s);
+  if (fmt == QW_FMT_INT4_G32) return launch_anch<QW_FMT_INT4_G32, DT>(a, s);
+  return launch_anch<QW_FMT_NF4_B64, DT>(a, s);
+}
+
+// Argument checks the two entry points share; fills the weights' and rows'
+// part of the arguments.
+qw_status check_experts(const qw_experts *ew, const void *X, qw_dtype x_dtype, const qw_groups *g,
+                        const void *Y, qw_dtype y_dtype, ExpertArgs *a) {
+  if (!ew || !X || !Y || !g || ew->E < 1) return QW_ERR_INVALID_ARG;
+  if (x_dtype != QW_DT_F16 && x_dtype != QW_DT_BF16) return QW_ERR_INVALID_ARG;
+  if (!is_dtype(y_dtype)) return QW_ERR_INVALID_ARG;
+  const qw_weight *w = &ew->w;
+  if (w->format != QW_FMT_2BIT_G32 && w->format != QW_FMT_NF4_B64 && w->format != QW_FMT_INT4_G32)
+    return QW_ERR_INVALID_ARG;
+  QW_TRY(check_weight_view(w, w->format, 0));
+  QW_TRY(check_groups(g));
+  if (g->G != ew->E) return QW_ERR_INVALID_ARG;
+  if (!aligned16(X) || !aligned16(Y)) return QW_ERR_ALIGNMENT;
+  if (w->K % 64 || (unsigned long long)w->N * w->K >= (1ull << 32)) return QW_ERR_UNSUPPORTED;
+  *a = ExpertArgs{};
+  a->X = reinterpret_cast<const uint16_t *>(X);
+  a->codes = w->codes;
+  a->scales = reinterpret_cast<const uint8_t *>(w->scales);
+  a->idx = w->out_idx;
+  a->mask = w->out_mask;
+  a->wo = w->out_w;
+  a->offsets = g->offsets;
+  a->rows = g->rows;
+  a->G = g->G;
+  a->n = g->n;
+  a->N = a->out_n = w->N;
+  a->K = w->K;
+  a->n_out = w->format == QW_FMT_NF4_B64 ? 0 : w->n_out;
+  a->n_out_pad = w->n_out_pad;
+  const float *L = nf4_levels_host();
+  for (int i = 0; i < 16; ++i) a->nf4[i] = L[i];
+  return QW_OK;
+}
+
+qw_status run_experts(const qw_experts *ew, qw_dtype x_dtype, ExpertArgs &a, hipStream_t s) {
+  const int cols = a.swiglu ? kCols / 2 : kCols;
+  a.col_tiles = (a.out_n + cols - 1) / cols;
+  return x_dtype == QW_DT_F16 ? launch_fmt<QW_DT_F16>(ew->w.format, a, s)
+                              : launch_fmt<QW_DT_BF16>(ew->w.format, a, s);
+}
+
+}  // namespace
+}  // namespace qw
+
+extern "C" {
+
+qw_status qgemm_experts(const qw_experts *ew, const void *X, qw_dtype x_dtype, int x_rows, int x_div,
+                        const qw_groups *g, int swiglu, void *Y, qw_dtype y_dtype, void *stream) {
+  using namespace qw;
+  CallScope scope;
+  ExpertArgs a;
+  QW_TRY(check_experts(ew, X, x_dtype, g, Y, y_dtype, &a));
+  if (x_rows < 1 || x_div < 0 || (x_div == 0 && x_rows < g->n)) return QW_ERR_INVALID_ARG;
+  if (swiglu && a.N % 2) return QW_ERR_INVALID_ARG;
+  QW_TRY(current_device(nullptr));
+  a.Y = Y;
+  a.x_rows = x_rows;
+  a.x_div = x_div;
+  a.swiglu = swiglu != 0;
+  if (a.swiglu) a.out_n = a.N / 2;
+  a.y_dtype = y_dtype;
+  return run_experts(ew, x_dtype, a, as_stream(stream));
+}
+
+size_t qw_experts_combine_workspace_bytes(int N, int T, int top_k) {
+  if (N < 1 || T < 1 || top_k < 1 || (long long)T * top_k > QW_MAX_ROWS) return 0;
+  return (size_t)T * (size_t)top_k * (size_t)N * sizeof(float);
+}
+
+qw_status qgemm_experts_combine(const qw_experts *ew, const void *H, qw_dtype h_dtype, const qw_groups *g,
+                                const int32_t *ids, const float *weights, int T, int top_k, void *out,
+                                qw_dtype out_dtype, void *workspace, size_t workspace_bytes, void *stream) {
+  using namespace qw;
+  CallScope scope;
+  ExpertArgs a;
+  QW_TRY(check_experts(ew, H, h_dtype, g, out, out_dtype, &a));
+  if (!ids || !weights || T < 1 || top_k < 1 || (long long)T * top_k != g->n) return QW_ERR_INVALID_ARG;
+  const size_t need = qw_experts_combine_workspace_bytes(a.N, T, top_k);
+  if (!workspace || workspace_bytes < need) return QW_ERR_INVALID_ARG;
+  if (!aligned16(ids) || !aligned16(weights) || !aligned16(workspace)) return QW_ERR_ALIGNMENT;
+  QW_TRY(current_device(nullptr));
+  const int col_blocks = (a.N + 1023) / 1024;
+  if ((long long)T * col_blocks >= (1ll << 31)) return QW_ERR_UNSUPPORTED;
+  a.Y = workspace;
+  a.x_rows = g->n;
+  a.x_div = 0;
+  a.by_slot = 1;
+  a.y_dtype = QW_DT_F32;
+  QW_TRY(run_experts(ew, h_dtype, a, as_stream(stream)));
+  CombineArgs c{reinterpret_cast<const float *>(workspace), ids, weights, out, T, top_k, a.N, ew->E, out_dtype, col_blocks};
+  QW_HIP_TRY(launch(combine_kernel, (unsigned)(T * col_blocks), 256, 0, as_stream(stream), c));
+  return QW_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,69 @@
+// Rows grouped by the matrix they take (qw_groups): the device-side lookup
+// shared by the kernels that walk tiles of grouped rows.
+#pragma once
+
+#include "qw_internal.h"
+
+namespace qw {
+
+// One tile of up to `height` rows of one group.
+struct RowTile {
+  int g;    // group
+  int p0;   // first position
+  int cnt;  // rows in the tile, 1..height; 0: there is no such tile
+};
+
+// Tile number `tile` of the tiles that cut every group into runs of up to
+// `height` positions, groups in order. Called by whole waves with
+// wave-uniform arguments; the result is wave-uniform. The offsets are
+// clamped to 0..n and a descending pair counts as an empty group, so the
+// positions of a tile lie in 0..n-1 whatever the arrays hold. With `rest`
+// the positions behind the last group count as one more group, number G.
+__device__ inline RowTile find_row_tile(const int32_t *offsets, int G, int n, int height, int tile,
+                                        bool rest = false) {
+  const int lane = threadIdx.x & 63;
+  const int groups = rest ? G + 1 : G;
+  int before = 0;  // tiles of the groups before this run of 64
+  for (int g0 = 0; g0 < groups; g0 += 64) {
+    const int g = g0 + lane;
+    int lo = 0, hi = 0;
+    if (g < groups) {
+      lo = min(max(offsets[g], 0), n);
+      hi = g < G ? min(max(offsets[g + 1], lo), n) : n;
+    }
+    const int own = (hi - lo + height - 1) / height;
+    int upto = own;  // inclusive prefix sum over the wave
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int v = __shfl_up(upto, d, 64);
+      if (lane >= d) upto += v;
+    }
+    const uint64_t past = __ballot(before + upto > tile);
+    if (past) {
+      const int f = __ffsll((unsigned long long)past) - 1;
+      const int first = before + __builtin_amdgcn_readlane(upto, f) - __builtin_amdgcn_readlane(own, f);
+      const int p0 = __builtin_amdgcn_readlane(lo, f) + (tile - first) * height;
+      const int end = __builtin_amdgcn_readlane(hi, f);
+      return RowTile{g0 + f, p0, min(height, end - p0)};
+    }
+    before += __builtin_amdgcn_readlane(upto, 63);
+  }
+  return RowTile{0, 0, 0};
+}
+
+// Most tiles that n rows in G groups can make: every group ends in at most
+// one short tile, and no tile is empty.
+inline long long most_row_tiles(int n, int G, int height) {
+  const long long full = (long long)n / height + G;
+  return full < n ? full : n;
+}
+
+// Validates a qw_groups view (sizes, NULLs, alignment).
+inline qw_status check_groups(const qw_groups *g) {
+  if (!g || g->G < 1 || g->n < 1 || !g->offsets || !g->rows) return QW_ERR_INVALID_ARG;
+  if (!aligned16(g->offsets) || !aligned16(g->rows)) return QW_ERR_ALIGNMENT;
+  if (g->G > QW_MAX_GROUPS || g->n > QW_MAX_ROWS) return QW_ERR_UNSUPPORTED;
+  return QW_OK;
+}
+
+}  // namespace qw

@@ -23,6 +23,7 @@ QW_STATIC_SCRATCH_BYTES = 8 << 20
 QW_FMT_2BIT_G32, QW_FMT_NF4_B64, QW_FMT_INT4_G32 = 1, 2, 3
 QW_DT_F16, QW_DT_BF16, QW_DT_F32 = 1, 2, 3
 QW_SCORE_MEANABS, QW_SCORE_L2 = 1, 2
+QW_MAX_GROUPS, QW_MAX_TOPK, QW_MAX_ROWS, QW_MAX_RANK = 1024, 32, 1 << 24, 256
 
 # every function declared in include/qw.h and include/qw_tuning.h
 EXPORTS = [
@@ -34,6 +35,9 @@ EXPORTS = [
     "qgemv_2bit", "qgemv_2bit_workspace_bytes", "qgemv_2bit_ws", "qgemv_2bit_static", "qgemv_nf4", "qgemv_int4",
     "qgemv_2bit_grouped", "qgemv_2bit_swiglu",
     "qgemm_prefill", "qw_tune_set", "qw_tune_get",
+    "qw_group_rows_workspace_bytes", "qw_group_rows", "qw_route_workspace_bytes", "qw_route_topk",
+    "qgemm_experts", "qw_experts_combine_workspace_bytes", "qgemm_experts_combine",
+    "qw_lora_workspace_bytes", "qw_lora_add",
 ]
 
 # test hooks (include/qw_tuning.h)
@@ -76,6 +80,23 @@ class qw_stack(ctypes.Structure):
     _fields_ = [
         ("plan", ctypes.c_void_p), ("n_stages", ctypes.c_int32), ("grid", ctypes.c_int32),
         ("lds", ctypes.c_int32),
+    ]
+
+
+class qw_groups(ctypes.Structure):
+    _fields_ = [
+        ("G", ctypes.c_int32), ("n", ctypes.c_int32), ("offsets", ctypes.c_void_p), ("rows", ctypes.c_void_p),
+    ]
+
+
+class qw_experts(ctypes.Structure):
+    _fields_ = [("E", ctypes.c_int32), ("w", qw_weight)]
+
+
+class qw_adapters(ctypes.Structure):
+    _fields_ = [
+        ("count", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32), ("r", ctypes.c_int32),
+        ("dtype", ctypes.c_int32), ("A", ctypes.c_void_p), ("B", ctypes.c_void_p), ("scale", ctypes.c_void_p),
     ]
 
 
@@ -127,6 +148,18 @@ def lib():
         "qgemv_2bit_grouped": (c_i, [W, c_i, c_p, c_i, ctypes.POINTER(c_p), c_i, c_p]),
         "qgemv_2bit_swiglu": (c_i, [W, c_p, c_i, c_p, c_i, c_p]),
         "qgemm_prefill": (c_i, [W, c_p, c_i, c_p, c_i, c_p]),
+        "qw_group_rows_workspace_bytes": (c_sz, [c_i, c_i]),
+        "qw_group_rows": (c_i, [c_p, c_i, c_i, c_p, c_p, c_p, c_sz, c_p]),
+        "qw_route_workspace_bytes": (c_sz, [c_i, c_i, c_i]),
+        "qw_route_topk": (c_i, [c_p, c_i, c_i, c_i, c_i, c_i, c_p, c_p, c_p, c_p, c_p, c_sz, c_p]),
+        "qgemm_experts": (c_i, [ctypes.POINTER(qw_experts), c_p, c_i, c_i, c_i, ctypes.POINTER(qw_groups), c_i,
+                                c_p, c_i, c_p]),
+        "qw_experts_combine_workspace_bytes": (c_sz, [c_i, c_i, c_i]),
+        "qgemm_experts_combine": (c_i, [ctypes.POINTER(qw_experts), c_p, c_i, ctypes.POINTER(qw_groups), c_p, c_p,
+                                        c_i, c_i, c_p, c_i, c_p, c_sz, c_p]),
+        "qw_lora_workspace_bytes": (c_sz, [ctypes.POINTER(qw_adapters), c_i]),
+        "qw_lora_add": (c_i, [ctypes.POINTER(qw_adapters), c_p, ctypes.POINTER(qw_groups), c_p, c_i, c_p, c_i,
+                              c_p, c_sz, c_p]),
         "qw_tune_set": (c_i, [c_i, c_i]),
         "qw_tune_get": (c_i, [c_i]),
     }
@@ -654,3 +687,263 @@ class Stack:
     def error(self):
         """Non-zero when a barrier wait of the last run gave up (synchronizes)."""
         return int(self.sync[0].item())
+
+
+# ------------------------------------------- rows that take different matrices
+
+def _same_device(*tensors):
+    """All tensors contiguous on the current device: the library launches
+    there, on the current stream."""
+    import torch
+    here = torch.cuda.current_device()
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda or not t.is_contiguous():
+            raise ValueError("tensors must be contiguous CUDA tensors")
+        if t.device.index != here:
+            raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{here}")
+
+
+def _bytes_of(t):
+    return t.numel() * t.element_size()
+
+
+def _need_bytes(t, nbytes, name):
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor")
+    if _bytes_of(t) != nbytes:
+        raise ValueError(f"{name} has {_bytes_of(t)} bytes, expected {nbytes}")
+
+
+def _workspace(workspace, nbytes, device):
+    """The caller's uint8 workspace, checked, or a new one where it is None."""
+    import torch
+    if workspace is None:
+        return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
+    _need(workspace, torch.uint8, "workspace")
+    if workspace.numel() < nbytes:
+        raise ValueError(f"workspace has {workspace.numel()} bytes, {nbytes} are needed")
+    return workspace
+
+
+class RowGroups:
+    """Rows grouped by the matrix they take (qw_groups): ``offsets`` int32
+    (G + 1,) and ``rows`` int32 (n,) CUDA tensors, referenced, not copied."""
+
+    def __init__(self, offsets, rows):
+        import torch
+        _need(offsets, torch.int32, "offsets", 1)
+        _need(rows, torch.int32, "rows", 1)
+        if offsets.numel() < 2 or rows.numel() < 1:
+            raise ValueError("offsets has G + 1 >= 2 entries, rows n >= 1")
+        self.offsets, self.rows = offsets, rows
+        self.G, self.n = offsets.numel() - 1, rows.numel()
+        self._c = qw_groups(self.G, self.n, offsets.data_ptr(), rows.data_ptr())
+
+
+class Routing:
+    """What qw_route_topk computes: ``ids`` int32 (T, k), ``weights`` fp32
+    (T, k) and ``groups``, the slots t * k + j grouped by expert."""
+
+    def __init__(self, ids, weights, groups):
+        self.ids, self.weights, self.groups = ids, weights, groups
+
+
+def qw_group_rows_workspace_bytes(n, G):
+    return int(lib().qw_group_rows_workspace_bytes(int(n), int(G)))
+
+
+def qw_group_rows(ids, G, workspace=None):
+    """RowGroups of the rows by ``ids`` (int32 (n,); ids outside 0..G-1 are in
+    no group)."""
+    import torch
+    _need(ids, torch.int32, "ids", 1)
+    n = ids.numel()
+    ws = _workspace(workspace, qw_group_rows_workspace_bytes(n, G), ids.device)
+    _same_device(ids, ws)
+    offsets = torch.empty(G + 1, dtype=torch.int32, device=ids.device)
+    rows = torch.empty(n, dtype=torch.int32, device=ids.device)
+    _check(lib().qw_group_rows(_ptr(ids), n, int(G), _ptr(offsets), _ptr(rows), _ptr(ws), ws.numel(), _stream()),
+           "qw_group_rows")
+    return RowGroups(offsets, rows)
+
+
+def qw_route_workspace_bytes(T, E, top_k):
+    return int(lib().qw_route_workspace_bytes(int(T), int(E), int(top_k)))
+
+
+def qw_route_topk(logits, top_k, normalize=True, workspace=None):
+    """The router: top_k experts of each row of logits (T, E; fp32, fp16 or
+    bf16), their softmax weights and the slots grouped by expert."""
+    import torch
+    dt = _need_any(logits, "logits", 2)
+    T, E = logits.shape
+    top_k = int(top_k)
+    ws = _workspace(workspace, qw_route_workspace_bytes(T, E, top_k), logits.device)
+    _same_device(logits, ws)
+    if not 1 <= top_k <= E:
+        raise ValueError("top_k must be in 1..E")
+    dev = logits.device
+    ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
+    weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
+    offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
+    rows = torch.empty(T * top_k, dtype=torch.int32, device=dev)
+    _check(lib().qw_route_topk(_ptr(logits), dt, T, E, top_k, 1 if normalize else 0, _ptr(ids), _ptr(weights),
+                               _ptr(offsets), _ptr(rows), _ptr(ws), ws.numel(), _stream()), "qw_route_topk")
+    return Routing(ids, weights, RowGroups(offsets, rows))
+
+
+class ExpertWeights:
+    """The packed weights of E experts of one shape, one behind another in
+    each buffer (qw_experts). Buffers that are given are referenced, not
+    copied; the others are allocated, uninitialised."""
+
+    def __init__(self, fmt, E, N, K, n_out=0, codes=None, scales=None, out_idx=None, out_w=None, out_mask=None,
+                 device="cuda"):
+        import torch
+        if E < 1:
+            raise ValueError("E must be positive")
+        z = qw_packed_sizes(fmt, N, K, n_out)
+        self.format, self.E, self.N, self.K, self.n_out, self.n_out_pad = fmt, E, N, K, n_out, z["n_out_pad"]
+        if fmt == QW_FMT_INT4_G32:
+            z["out_idx"] = 0  # the products do not read the permutation
+        for name, given in (("codes", codes), ("scales", scales), ("out_idx", out_idx), ("out_w", out_w),
+                            ("out_mask", out_mask)):
+            nb = E * z[name]
+            if nb == 0:
+                t = None
+            elif given is not None:
+                _need_bytes(given, nb, name)
+                t = given
+            else:
+                t = torch.empty(nb, dtype=torch.uint8, device=device)
+                t = t.view(torch.int16) if name == "out_w" else t.view(torch.int32) if name.startswith("out_") else t
+            setattr(self, name, t)
+        p = lambda t: t.data_ptr() if t is not None else None
+        self._c = qw_experts(E, qw_weight(fmt, N, K, n_out, self.n_out_pad, p(self.codes), p(self.scales),
+                                          p(self.out_idx), p(self.out_w), p(self.out_mask)))
+
+    @classmethod
+    def stack(cls, packed):
+        """Copies of PackedWeight matrices of one format, shape and anchor
+        count as the experts 0, 1, ..."""
+        import torch
+        a = packed[0]
+        if any((p.format, p.N, p.K, p.n_out) != (a.format, a.N, a.K, a.n_out) for p in packed):
+            raise ValueError("experts have one format, shape and number of anchors")
+        cat = lambda name: None if getattr(a, name) is None else torch.cat([getattr(p, name) for p in packed])
+        return cls(a.format, len(packed), a.N, a.K, a.n_out, cat("codes"), cat("scales"),
+                   None if a.format == QW_FMT_INT4_G32 else cat("out_idx"), cat("out_w"), cat("out_mask"))
+
+    def nbytes(self):
+        return sum(_bytes_of(t) for t in (self.codes, self.scales, self.out_idx, self.out_w, self.out_mask)
+                   if t is not None)
+
+
+def _experts_x(ew, x, name):
+    import torch
+    if x.dtype not in (torch.float16, torch.bfloat16):
+        raise TypeError(f"{name} must be fp16 or bf16, got {x.dtype}")
+    if x.dim() != 2 or x.shape[1] != ew.K:
+        raise ValueError(f"{name} has shape {tuple(x.shape)}, the experts' K is {ew.K}")
+
+
+def qgemm_experts(ew, X, groups, top_k=1, swiglu=False, out_dtype=None, out=None):
+    """Y[p] = X[rows[p] // top_k] . W_e^T for every position p of groups
+    (RowGroups), e its group; top_k=None: X is in grouped order (row p).
+    swiglu: silu(gate) * up of merged gate/up experts. Rows of ``out`` that
+    are in no group are left as they were."""
+    import torch
+    _experts_x(ew, X, "X")
+    if groups.G != ew.E:
+        raise ValueError(f"{groups.G} groups, {ew.E} experts")
+    if swiglu and ew.N % 2:
+        raise ValueError("merged gate/up experts have N = 2I rows")
+    N = ew.N // 2 if swiglu else ew.N
+    div = 0 if top_k is None else int(top_k)
+    if top_k is not None and (div < 1 or (groups.n + div - 1) // div > X.shape[0]):
+        raise ValueError(f"{groups.n} slots of {top_k} a row need more than the {X.shape[0]} rows of X")
+    if top_k is None and X.shape[0] < groups.n:
+        raise ValueError(f"X has {X.shape[0]} rows, the groups {groups.n}")
+    Y = out if out is not None else torch.empty((groups.n, N), dtype=out_dtype or X.dtype, device=X.device)
+    if tuple(Y.shape) != (groups.n, N):
+        raise ValueError(f"output shape {tuple(Y.shape)}, expected {(groups.n, N)}")
+    _same_device(X, Y, groups.offsets, groups.rows, ew.codes)
+    _check(lib().qgemm_experts(ctypes.byref(ew._c), _ptr(X), _dt(X.dtype), X.shape[0], div, ctypes.byref(groups._c),
+                               1 if swiglu else 0, _ptr(Y), _dt(Y.dtype), _stream()), "qgemm_experts")
+    return Y
+
+
+def qw_experts_combine_workspace_bytes(N, T, top_k):
+    return int(lib().qw_experts_combine_workspace_bytes(int(N), int(T), int(top_k)))
+
+
+def qgemm_experts_combine(ew, H, groups, ids, weights, out_dtype=None, out=None, workspace=None):
+    """out[t] = sum_j weights[t, j] * (H[position of slot (t, j)] . W_e^T),
+    e = ids[t, j]: the down projections of a routed layer, H (T * k, K) in
+    grouped order, summed per token."""
+    import torch
+    _experts_x(ew, H, "H")
+    _need(ids, torch.int32, "ids", 2)
+    _need(weights, torch.float32, "weights", 2)
+    T, k = ids.shape
+    if groups.G != ew.E or groups.n != T * k or tuple(weights.shape) != (T, k) or H.shape[0] != T * k:
+        raise ValueError("groups, ids, weights and H must describe the same T * top_k slots of the experts")
+    Y = out if out is not None else torch.empty((T, ew.N), dtype=out_dtype or H.dtype, device=H.device)
+    if tuple(Y.shape) != (T, ew.N):
+        raise ValueError(f"output shape {tuple(Y.shape)}, expected {(T, ew.N)}")
+    ws = _workspace(workspace, qw_experts_combine_workspace_bytes(ew.N, T, k), H.device)
+    _same_device(H, Y, ids, weights, ws, groups.offsets, groups.rows, ew.codes)
+    _check(lib().qgemm_experts_combine(ctypes.byref(ew._c), _ptr(H), _dt(H.dtype), ctypes.byref(groups._c), _ptr(ids),
+                                       _ptr(weights), T, k, _ptr(Y), _dt(Y.dtype), _ptr(ws), ws.numel(), _stream()),
+           "qgemm_experts_combine")
+    return Y
+
+
+class Adapters:
+    """Low-rank adapters of one projection (qw_adapters): A (count, r, K) and
+    B (count, N, r), fp16 or bf16, and scale (count,) fp32 CUDA tensors,
+    referenced, not copied. Adapters of a smaller rank are padded with zeros."""
+
+    def __init__(self, A, B, scale):
+        import torch
+        if A.dtype not in (torch.float16, torch.bfloat16) or B.dtype != A.dtype:
+            raise TypeError("A and B must both be fp16 or both bf16")
+        _need(A, A.dtype, "A", 3)
+        _need(B, A.dtype, "B", 3)
+        _need(scale, torch.float32, "scale", 1)
+        self.count, self.r, self.K = A.shape
+        self.N = B.shape[1]
+        if B.shape[0] != self.count or B.shape[2] != self.r or scale.numel() != self.count:
+            raise ValueError("A (count, r, K), B (count, N, r) and scale (count,) do not fit together")
+        self.A, self.B, self.scale, self.dtype = A, B, scale, A.dtype
+        self._c = qw_adapters(self.count, self.N, self.K, self.r, _dt(A.dtype), A.data_ptr(), B.data_ptr(),
+                              scale.data_ptr())
+
+
+def qw_lora_workspace_bytes(adapters, n):
+    return int(lib().qw_lora_workspace_bytes(ctypes.byref(adapters._c), int(n)))
+
+
+def qw_lora_add(adapters, x, groups, base, out_dtype=None, out=None, workspace=None):
+    """out[m] = base[m] + scale[a] * B_a (A_a x[m]) for the rows m of groups
+    (RowGroups by adapter); rows of no group get base[m]. ``base`` is the
+    shared projection's output (any of the three types); out=base adds in
+    place."""
+    import torch
+    _need(x, adapters.dtype, "x", 2)
+    n = x.shape[0]
+    if x.shape[1] != adapters.K or tuple(base.shape) != (n, adapters.N):
+        raise ValueError(f"x {tuple(x.shape)} and base {tuple(base.shape)} do not fit K = {adapters.K}, N = {adapters.N}")
+    if groups.G != adapters.count or groups.n != n:
+        raise ValueError(f"groups of {groups.n} rows by {groups.G}, expected {n} by {adapters.count}")
+    Y = out if out is not None else torch.empty((n, adapters.N), dtype=out_dtype or base.dtype, device=x.device)
+    if tuple(Y.shape) != (n, adapters.N):
+        raise ValueError(f"output shape {tuple(Y.shape)}, expected {(n, adapters.N)}")
+    ws = _workspace(workspace, qw_lora_workspace_bytes(adapters, n), x.device)
+    _same_device(x, base, Y, ws, groups.offsets, groups.rows, adapters.A, adapters.B, adapters.scale)
+    _check(lib().qw_lora_add(ctypes.byref(adapters._c), _ptr(x), ctypes.byref(groups._c), _ptr(base), _dt(base.dtype),
+                             _ptr(Y), _dt(Y.dtype), _ptr(ws), ws.numel(), _stream()), "qw_lora_add")
+    return Y

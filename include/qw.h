@@ -503,6 +503,174 @@ qw_status qw_stack_run(const qw_stack *st, uint32_t *sync, void *stream);
 qw_status qgemm_prefill(const qw_weight *w, const void *X, int M, void *Y,
                         qw_dtype y_dtype, void *stream);
 
+/* ---- rows that take different matrices -----------------------------------
+ *
+ * The products above apply one matrix to every row of a batch. The calls
+ * below serve batches whose rows take different ones: the experts of a
+ * routed layer, or the low-rank adapters of many requests beside one shared
+ * projection. (The OTF-LLM page names neither; its per-token streaming
+ * argument, section 1, is theirs too: a matrix that some row takes should
+ * be read once for all rows that take it.) They share one description of
+ * which row takes which matrix: the rows in the order of their matrices. */
+
+/* Largest number of groups (experts or adapters) of one call. */
+#define QW_MAX_GROUPS 1024
+/* Largest top_k of qw_route_topk. */
+#define QW_MAX_TOPK 32
+/* Largest number of grouped rows of one call (T * top_k for a router). */
+#define QW_MAX_ROWS (1 << 24)
+
+/* Rows grouped by the matrix they take. Group g holds the rows
+ * rows[offsets[g]] .. rows[offsets[g+1] - 1]; the rows from position
+ * offsets[G] on take none. offsets is ascending with offsets[0] = 0 and
+ * offsets[G] <= n; rows is a permutation of 0..n-1. Both are what
+ * qw_group_rows and qw_route_topk write. The contents are device data that
+ * no call checks on the host: offsets are clamped to 0..n and rows outside
+ * their range are skipped, so wrong contents give wrong values but no
+ * access out of bounds. */
+typedef struct {
+  int32_t G;              /* number of groups, 1..QW_MAX_GROUPS */
+  int32_t n;              /* number of rows, 1..QW_MAX_ROWS */
+  const int32_t *offsets; /* device int32 [G+1] */
+  const int32_t *rows;    /* device int32 [n] */
+} qw_groups;
+
+/* Device workspace bytes of qw_group_rows for n rows and G groups (0 when
+ * none is needed or an argument is out of range). Host only. */
+size_t qw_group_rows_workspace_bytes(int n, int G);
+
+/* Groups rows by id: row i belongs to group ids[i], or to none when ids[i]
+ * is outside 0..G-1 (-1 by convention). Rows of one group keep their order;
+ * rows of no group follow behind the last group, in order.
+ *   ids     device int32 [n], n >= 1
+ *   offsets device int32 [G+1], rows device int32 [n]: the qw_groups arrays
+ *   workspace device scratch of workspace_bytes >=
+ *           qw_group_rows_workspace_bytes(n, G); calls that overlap in time
+ *           must not share it. Its contents on entry do not matter.
+ * Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED (G > QW_MAX_GROUPS, n >
+ * QW_MAX_ROWS), HIP. */
+qw_status qw_group_rows(const int32_t *ids, int n, int G, int32_t *offsets,
+                        int32_t *rows, void *workspace, size_t workspace_bytes,
+                        void *stream);
+
+/* Device workspace bytes of qw_route_topk (0 when none is needed or an
+ * argument is out of range). Host only. */
+size_t qw_route_workspace_bytes(int T, int E, int top_k);
+
+/* The router of a layer of experts: the top_k largest of each token's E
+ * logits, their softmax weights, and the T * top_k (token, choice) slots
+ * grouped by expert.
+ *   logits  device [T][E] of dtype F32, F16 or BF16. -inf marks an expert
+ *           the token may not take; NaN is taken as -inf.
+ *   ids     device int32 [T][top_k]: the chosen experts, largest logit
+ *           first, equal logits by the lower expert; -1 where fewer than
+ *           top_k logits are above -inf.
+ *   weights device fp32 [T][top_k]: exp(l - max) / sum, the sum over the
+ *           chosen experts (normalize != 0) or over all E; 0 where the id
+ *           is -1.
+ *   offsets device int32 [E+1], rows device int32 [T * top_k]: the slots
+ *           t * top_k + j grouped by ids[t][j], as qw_group_rows leaves them.
+ * The exponentials and their sum are fp32. 1 <= top_k <= min(E,
+ * QW_MAX_TOPK). Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED (E >
+ * QW_MAX_GROUPS, T * top_k > QW_MAX_ROWS), HIP. */
+qw_status qw_route_topk(const void *logits, qw_dtype dtype, int T, int E,
+                        int top_k, int normalize, int32_t *ids, float *weights,
+                        int32_t *offsets, int32_t *rows, void *workspace,
+                        size_t workspace_bytes, void *stream);
+
+/* The packed weights of E experts of one shape. w is the view of expert 0;
+ * its buffers hold the experts one behind another: codes [E][N][...],
+ * scales [E][N][...], out_idx [E][n_out] and out_mask [E][K/32] (2-bit with
+ * anchors), out_w [E][N][n_out_pad]. All experts have the same number of
+ * anchors. INT4: one channel permutation for all experts (the activations
+ * come in its order); out_idx is not read. */
+typedef struct {
+  int32_t E;   /* experts, 1..QW_MAX_GROUPS */
+  qw_weight w; /* expert 0; the others follow in the same buffers */
+} qw_experts;
+
+/* The products of the experts, every group of rows with its expert's
+ * weights (w_hat as in qgemv_2bit, qgemv_nf4 and qgemv_int4, anchors
+ * included):
+ *   Y[p][n] = sum_k X[r(p)][k] w_hat_e[n][k],   e the group of position p,
+ * for every position p of a group; r(p) = rows[p] / x_div, or r(p) = p when
+ * x_div is 0 (X already in grouped order). With the slots of qw_route_topk,
+ * x_div = top_k takes each slot's token. swiglu != 0: N = 2I, the gate rows
+ * 0..I-1 over the up rows, and Y[p][n] = silu(g) * u as in
+ * qgemv_2bit_swiglu, Y being [n][I].
+ *   X  device [x_rows][K] of x_dtype F16 or BF16 (x_rows >= g->n when x_div
+ *      is 0); g->G == ew->E
+ *   Y  device [g->n][N or I] of y_dtype F16, BF16 or F32, rounded once;
+ *      rows of positions in no group are left as they were.
+ * fp32 accumulation. Where the rows per expert are few (n < 32 E) the
+ * weights enter the products to 16 bits or better, else rounded to x_dtype
+ * as in qgemm_prefill; weights beyond x_dtype's range (F16: 65504) are then
+ * infinite. K must be a multiple of 64 and N K below 2^32. No workspace.
+ * Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED, HIP. */
+qw_status qgemm_experts(const qw_experts *ew, const void *X, qw_dtype x_dtype,
+                        int x_rows, int x_div, const qw_groups *g, int swiglu,
+                        void *Y, qw_dtype y_dtype, void *stream);
+
+/* Device workspace bytes of qgemm_experts_combine: the fp32 products of the
+ * T * top_k slots (0 when an argument is out of range). Host only. */
+size_t qw_experts_combine_workspace_bytes(int N, int T, int top_k);
+
+/* The experts' products summed per token (a routed layer's down
+ * projection):
+ *   out[t][n] = sum_j weights[t][j] * y(t, j)[n],
+ * y(t, j) the product of slot t * top_k + j with the weights of its expert
+ * ids[t][j], over the j whose id is in 0..E-1; a token without any gives
+ * zeros. The products and the sum (in the order of j) are fp32, rounded
+ * once to out's type.
+ *   H   device [T * top_k][K] of h_dtype F16 or BF16, in grouped order (row
+ *       p is position p of g, as qgemm_experts writes it); g->n = T * top_k
+ *   ids, weights: as qw_route_topk writes them; g must be grouped by ids
+ *   out device [T][N] of out_dtype F16, BF16 or F32
+ *   workspace device scratch, workspace_bytes >=
+ *       qw_experts_combine_workspace_bytes(N, T, top_k)
+ * Conventions and errors as qgemm_experts. */
+qw_status qgemm_experts_combine(const qw_experts *ew, const void *H, qw_dtype h_dtype,
+                                const qw_groups *g, const int32_t *ids,
+                                const float *weights, int T, int top_k, void *out,
+                                qw_dtype out_dtype, void *workspace,
+                                size_t workspace_bytes, void *stream);
+
+/* The low-rank adapters of many requests beside one projection of N outputs
+ * and K inputs: adapter a adds scale[a] * B_a (A_a x) to its rows. */
+typedef struct {
+  int32_t count;      /* adapters, 1..QW_MAX_GROUPS */
+  int32_t N, K, r;    /* K and r multiples of 8, 8 <= r <= QW_MAX_RANK */
+  int32_t dtype;      /* QW_DT_F16 or QW_DT_BF16, of A and B */
+  const void *A;      /* device [count][r][K] */
+  const void *B;      /* device [count][N][r] */
+  const float *scale; /* device fp32 [count] */
+} qw_adapters;
+
+/* Largest adapter rank. */
+#define QW_MAX_RANK 256
+
+/* Device workspace bytes of qw_lora_add for n rows (0 when an argument is
+ * out of range). Host only. */
+size_t qw_lora_workspace_bytes(const qw_adapters *ad, int n);
+
+/* Adds each row's adapter to the output of a shared projection:
+ *   out[m] = base[m] + scale[a] * B_a (A_a x[m]),   a the group of row m,
+ * for every row of a group, rounded once to out's type; rows of no group
+ * get base[m]. base may be a projection's fp32 output, so that the sum is
+ * rounded once, and base == out (equal types) adds in place.
+ *   x    device [n][K] of ad->dtype, n = g->n; g->G == ad->count
+ *   base device [n][N] of base_dtype, out device [n][N] of out_dtype (F16,
+ *        BF16 or F32 each)
+ *   workspace device scratch of workspace_bytes >=
+ *        qw_lora_workspace_bytes(ad, n): the rows' r inner values in fp32
+ * A x and B (A x) accumulate in fp32, the inner values enter the second
+ * product to 16 bits or better. Errors: INVALID_ARG (out overlapping base
+ * with another type is not checked), ALIGNMENT, UNSUPPORTED, HIP. */
+qw_status qw_lora_add(const qw_adapters *ad, const void *x, const qw_groups *g,
+                      const void *base, qw_dtype base_dtype, void *out,
+                      qw_dtype out_dtype, void *workspace, size_t workspace_bytes,
+                      void *stream);
+
 #ifdef __cplusplus
 }
 #endif
