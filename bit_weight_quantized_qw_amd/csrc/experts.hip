@@ -27,8 +27,7 @@
 // 4-bit codes); the matrix instruction wants eight per lane of 32
 // consecutive ones. A 4 x 4 transposition of dwords over the four lane
 // groups (two half-wave and two row swaps) turns one into the other.
-#include "op16.h"
-#include "row_groups.h"
+#include "experts.h"
 
 namespace qw {
 namespace {
@@ -39,87 +38,6 @@ constexpr int kSub = kCols / 16;  // 16-column blocks of a tile
 constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
 constexpr int kChunk = 256;       // weights of one column in one set of loads
-
-struct ExpertArgs {
-  const uint16_t *X;        // [x_rows][K]
-  const uint8_t *codes;
-  const uint8_t *scales;
-  const int32_t *idx;       // 2-bit anchors [E][n_out]
-  const uint32_t *mask;     // 2-bit anchors [E][K/32]
-  const uint16_t *wo;       // anchors [E][N][n_out_pad], fp16
-  const int32_t *offsets, *rows;
-  void *Y;
-  int x_rows, x_div;
-  int G, n;                 // groups, positions
-  int N, K, out_n;          // weight rows, weight columns, columns of Y
-  int n_out, n_out_pad;
-  int col_tiles;
-  int swiglu, by_slot;      // by_slot: Y row rows[p] in place of p
-  int y_dtype;
-  float nf4[16];
-};
-
-__device__ inline __amdgpu_buffer_rsrc_t rsrc(const void *p, uint32_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), (short)0, (int)bytes, 0x00020000);
-}
-constexpr uint32_t kOob = 0x80000000u;  // an offset past every buffer's end (reads 0)
-
-__device__ inline void swap32(uint32_t &a, uint32_t &b) {
-  const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
-  a = r[0];
-  b = r[1];
-}
-__device__ inline void swap16(uint32_t &a, uint32_t &b) {
-  const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
-  a = r[0];
-  b = r[1];
-}
-// d[i] of lane group g (lanes 16g..16g+15) <-> d[g] of lane group i
-__device__ inline void transpose4(uint32_t (&d)[4]) {
-  swap32(d[0], d[2]);
-  swap32(d[1], d[3]);
-  swap16(d[0], d[1]);
-  swap16(d[2], d[3]);
-}
-// w of lane group i to all four lane groups, as out[i]
-__device__ inline void gather4(uint32_t w, uint32_t (&out)[4]) {
-  uint32_t a = w, b = w;
-  swap32(a, b);  // a: groups 0 1 0 1, b: groups 2 3 2 3
-  out[0] = out[1] = a;
-  out[2] = out[3] = b;
-  swap16(out[0], out[1]);
-  swap16(out[2], out[3]);
-}
-
-// Level table: entry of code byte v, replica r. 2-bit: four levels (8
-// bytes), INT4: two (4 bytes, two replicas side by side), NF4: the nearest
-// two and the rests of both (8 bytes).
-constexpr int kEntry = 128;  // bytes of one byte's replicas
-template <int FMT, int DT>
-__device__ inline void fill_table(char *tab, const ExpertArgs &a) {
-  for (int i = threadIdx.x; i < 256 * 8; i += kThreads) {
-    const int v = i >> 3;
-    u32x2 w;
-    if (FMT == QW_FMT_2BIT_G32) {
-      uint32_t l[4];
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const int q = (v >> (2 * t)) & 3;
-        l[t] = Op<DT>::bits(q == 0 ? -152.0f : q == 1 ? -45.0f : q == 2 ? 45.0f : 152.0f);
-      }
-      w = u32x2{l[0] | (l[1] << 16), l[2] | (l[3] << 16)};
-    } else if (FMT == QW_FMT_INT4_G32) {
-      const uint32_t p = Op<DT>::bits((float)((v & 15) - 8)) | (Op<DT>::bits((float)((v >> 4) - 8)) << 16);
-      w = u32x2{p, p};
-    } else {
-      const float lo = a.nf4[v & 15], hi = a.nf4[v >> 4];
-      const uint32_t lo16 = Op<DT>::bits(lo), hi16 = Op<DT>::bits(hi);
-      w = u32x2{lo16 | (hi16 << 16),
-                Op<DT>::bits(lo - Op<DT>::value(lo16)) | (Op<DT>::bits(hi - Op<DT>::value(hi16)) << 16)};
-    }
-    *reinterpret_cast<u32x4 *>(tab + v * kEntry + (i & 7) * 16) = u32x4{w[0], w[1], w[0], w[1]};
-  }
-}
 
 // The tile's gathered loads of one chunk: codes and scale words of the
 // lane's 64 weights in each of the four 16-column blocks.
@@ -145,7 +63,7 @@ __global__ __launch_bounds__(kThreads) void experts_kernel(ExpertArgs a) {
   if (rt.cnt == 0) return;
   const int e = rt.g, K = a.K;
 
-  fill_table<FMT, DT>(tab, a);
+  fill_table<FMT, DT, kThreads>(tab, a);
 
   // this lane's row of A: rows past the tile's end repeat its first row
   // (their products are not stored)
@@ -210,7 +128,7 @@ __global__ __launch_bounds__(kThreads) void experts_kernel(ExpertArgs a) {
 #pragma unroll
   for (int j = 0; j < kSub; ++j) acc[j] = f32x4{0, 0, 0, 0};
   const f32x4 zero = {0, 0, 0, 0};
-  const uint32_t rep = (uint32_t)(lane & 15) * 8u;
+  const uint32_t rep = FMT == QW_FMT_INT4_G32 ? (uint32_t)(lane & 31) * 4u : (uint32_t)(lane & 15) * 8u;
   auto entry = [&](uint32_t byte) { return tab + ((byte << 7) | rep); };
 
   // products of the eight 32-weight steps of a chunk
@@ -219,15 +137,7 @@ __global__ __launch_bounds__(kThreads) void experts_kernel(ExpertArgs a) {
     const int steps = min(8, (K - k0) / 32);
 #pragma unroll
     for (int j = 0; j < kSub; ++j) {
-      if (FMT == QW_FMT_2BIT_G32) {
-        // halves h0..h7 of the lane's 64 codes: dword g gets (h_g, h_4+g),
-        // so lane group g ends up with its 8 codes of steps 2s and 2s + 1
-        const uint32_t d0 = d.c[j][0], d1 = d.c[j][1], d2 = d.c[j][2], d3 = d.c[j][3];
-        d.c[j][0] = __builtin_amdgcn_perm(d2, d0, 0x05040100u);
-        d.c[j][1] = __builtin_amdgcn_perm(d2, d0, 0x07060302u);
-        d.c[j][2] = __builtin_amdgcn_perm(d3, d1, 0x05040100u);
-        d.c[j][3] = __builtin_amdgcn_perm(d3, d1, 0x07060302u);
-      }
+      if (FMT == QW_FMT_2BIT_G32) to_halves(reinterpret_cast<uint32_t(&)[4]>(d.c[j][0]));
 #pragma unroll
       for (int i = 0; i < CH::kCodes; i += 4)
         transpose4(reinterpret_cast<uint32_t(&)[4]>(d.c[j][i]));
@@ -337,15 +247,7 @@ __global__ __launch_bounds__(kThreads) void experts_kernel(ExpertArgs a) {
         u32x4 B = {0, 0, 0, 0}, B2 = {0, 0, 0, 0};
         if (wn[j] >= 0 && o < a.n_out_pad) {
           B = *reinterpret_cast<const u32x4 *>(a.wo + ((size_t)e * a.N + wn[j]) * a.n_out_pad + o);
-          if (DT == QW_DT_BF16) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const float lo = f16_bits_to_f32((uint16_t)B[q]), hi = f16_bits_to_f32((uint16_t)(B[q] >> 16));
-              const uint32_t lo16 = O::bits(lo), hi16 = O::bits(hi);
-              B[q] = lo16 | (hi16 << 16);
-              B2[q] = O::bits(lo - O::value(lo16)) | (O::bits(hi - O::value(hi16)) << 16);
-            }
-          }
+          if (DT == QW_DT_BF16) split_f16(B, B2);
         }
         acc[j] = O::mma(A, B, acc[j]);
         if (DT == QW_DT_BF16) acc[j] = O::mma(A, B2, acc[j]);
@@ -468,6 +370,16 @@ qw_status launch_fmt(int fmt, const ExpertArgs &a, hipStream_t s) {
   return launch_anch<QW_FMT_NF4_B64, DT>(a, s);
 }
 
+// 16-row blocks of a tile, from the mean number of rows of an expert.
+// 16 experts of 4096 x 2048 in 2-bit, us by the narrow kernel / tiles of 32
+// / of 64 rows: 8 rows an expert 27 / 37 / 46, 16: 40 / 39 / 48, 32: 58 / 49
+// / 66, 64: 100 / 78 / 68, 128: 177 / 117 / 100. Tiles of 128 rows leave
+// one wave a SIMD and were slower throughout (512 rows: 496 against 266).
+int row_blocks(int n, int G) {
+  const int mean = n / G;
+  return mean < 16 ? 1 : mean < 48 ? 2 : 4;
+}
+
 // Argument checks the two entry points share; fills the weights' and rows'
 // part of the arguments.
 qw_status check_experts(const qw_experts *ew, const void *X, qw_dtype x_dtype, const qw_groups *g,
@@ -504,6 +416,10 @@ qw_status check_experts(const qw_experts *ew, const void *X, qw_dtype x_dtype, c
 }
 
 qw_status run_experts(const qw_experts *ew, qw_dtype x_dtype, ExpertArgs &a, hipStream_t s) {
+  int blocks = row_blocks(a.n, a.G);
+  const int forced = tune(QW_TUNE_EXPERTS_ROW_BLOCKS);
+  if (forced >= 1) blocks = forced;
+  if (blocks > 1) return launch_experts_wide(ew->w.format, x_dtype, blocks, a, s);
   const int cols = a.swiglu ? kCols / 2 : kCols;
   a.col_tiles = (a.out_n + cols - 1) / cols;
   return x_dtype == QW_DT_F16 ? launch_fmt<QW_DT_F16>(ew->w.format, a, s)

@@ -51,6 +51,18 @@ __device__ inline RowTile find_row_tile(const int32_t *offsets, int G, int n, in
   return RowTile{0, 0, 0};
 }
 
+// Number of those tiles, wave-uniform.
+__device__ inline int count_row_tiles(const int32_t *offsets, int G, int n, int height) {
+  int own = 0;
+  for (int g = threadIdx.x & 63; g < G; g += 64) {
+    const int lo = min(max(offsets[g], 0), n);
+    own += (min(max(offsets[g + 1], lo), n) - lo + height - 1) / height;
+  }
+#pragma unroll
+  for (int d = 32; d; d >>= 1) own += __shfl_xor(own, d, 64);
+  return __builtin_amdgcn_readfirstlane(own);
+}
+
 // Most tiles that n rows in G groups can make: every group ends in at most
 // one short tile, and no tile is empty.
 inline long long most_row_tiles(int n, int G, int height) {

@@ -602,10 +602,11 @@ typedef struct {
  *      is 0); g->G == ew->E
  *   Y  device [g->n][N or I] of y_dtype F16, BF16 or F32, rounded once;
  *      rows of positions in no group are left as they were.
- * fp32 accumulation. Where the rows per expert are few (n < 32 E) the
- * weights enter the products to 16 bits or better, else rounded to x_dtype
- * as in qgemm_prefill; weights beyond x_dtype's range (F16: 65504) are then
- * infinite. K must be a multiple of 64 and N K below 2^32. No workspace.
+ * fp32 accumulation. The weights' scales multiply fp32 sums of code levels,
+ * so no weight is rounded to x_dtype; the NF4 levels are, to two numbers of
+ * it (n < 16 E) or to one after a common factor (n >= 16 E: at most half a
+ * step off, a third of that in the mean). K must be a multiple of 64
+ * and N K below 2^32. No workspace.
  * Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED, HIP. */
 qw_status qgemm_experts(const qw_experts *ew, const void *X, qw_dtype x_dtype,
                         int x_rows, int x_div, const qw_groups *g, int swiglu,

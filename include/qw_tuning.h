@@ -40,7 +40,10 @@ typedef enum {
   QW_TUNE_PREFILL_WIDE_TILES = 5,
   /* INT4 GEMV kernel: -1 / 0 the matrix-core kernel wherever it takes the
    * shape, 1 the vector-ALU kernel. */
-  QW_TUNE_INT4_PATH = 6
+  QW_TUNE_INT4_PATH = 6,
+  /* Experts' products: -1 / 0 automatic, 1 the narrow kernel (16 rows), 2 or
+   * 4 the wide one with tiles of that many 16-row blocks. */
+  QW_TUNE_EXPERTS_ROW_BLOCKS = 7
 } qw_tune_key;
 
 #define QW_TUNE_AUTO (-1)

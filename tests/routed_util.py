@@ -80,11 +80,14 @@ def device_groups(ids, G):
 
 def products(ex, x64, off, wide, dtype):
     """(values, bounds) of the rows in grouped order: row p times its group's
-    weights; wide: the weights are rounded to dtype first."""
+    weights; wide: by the kernel of wide tiles."""
     y = np.zeros((x64.shape[0], ex.N))
     tol = np.zeros_like(y)
-    # 2^-16: an NF4 level as two bf16 numbers (fp16: 2^-22); wide: one rounding
-    extra = half_step(dtype) if wide else half_step(dtype) ** 2 if ex.fmt == "nf4" else 0.0
+    extra = 0.0
+    if ex.fmt == "nf4":  # a level is two numbers of dtype, in wide tiles one
+        extra = half_step(dtype) if wide else half_step(dtype) ** 2
+    elif ex.fmt == "2bit" and wide:  # Z and the group sums of x as two bf16 numbers, without the product of the rests
+        extra = 2.0 ** -15
     for e in range(ex.E):
         s = slice(off[e], off[e + 1])
         y[s] = x64[s] @ ex.W[e].T

@@ -13,8 +13,9 @@ pytestmark = pytest.mark.gpu
 
 
 def is_wide(n, E):
-    """Whether the weights enter rounded to the activations' type (qw.h)."""
-    return n >= 32 * E
+    """Whether the call takes the kernel of wide tiles."""
+    forced = qw.qw_tune_get(qw.QW_TUNE_EXPERTS_ROW_BLOCKS)
+    return forced > 1 if forced > 0 else n // E >= 16
 
 
 def acts(rng, rows, K, dt):
@@ -70,8 +71,11 @@ def test_few_rows(fmt, n_out, dtype, N, K):
 @pytest.mark.parametrize("fmt,n_out", FORMATS)
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
 @pytest.mark.parametrize("N,K", [(40, 192), (260, 448), (300, 1024)])
-def test_many_rows(fmt, n_out, dtype, N, K):
-    """Some hundred rows an expert, unevenly."""
+@pytest.mark.parametrize("blocks", [None, 1, 2, 4])
+def test_many_rows(fmt, n_out, dtype, N, K, blocks, tune):
+    """Some hundred rows an expert, unevenly, by every tile height."""
+    if blocks:
+        tune(qw.QW_TUNE_EXPERTS_ROW_BLOCKS, blocks)
     ex = Experts(fmt, 3, N, K, n_out, seed=N)
     for T, k in ((48, 2), (331, 2), (701, 1)):
         check(ex, T, k, dtype, seed=T)
@@ -81,7 +85,10 @@ def test_many_rows(fmt, n_out, dtype, N, K):
 @pytest.mark.parametrize("fmt,n_out", FORMATS)
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
 @pytest.mark.parametrize("T,k", [(1, 2), (9, 3), (200, 3)])
-def test_gated(fmt, n_out, dtype, T, k):
+@pytest.mark.parametrize("blocks", [None, 1, 2, 4])
+def test_gated(fmt, n_out, dtype, T, k, blocks, tune):
+    if blocks:
+        tune(qw.QW_TUNE_EXPERTS_ROW_BLOCKS, blocks)
     for N, K in ((2, 64), (66, 256), (250, 640)):
         ex = Experts(fmt, 4, N, K, n_out, seed=N)
         check(ex, T, k, dtype, swiglu=True, seed=T)
@@ -96,8 +103,10 @@ def test_grouped_input_and_other_output_types(fmt, n_out, T, k):
     check(ex, T, k, "bf16", out="f16", seed=2, grouped=True)
 
 
-def test_long_rows_and_many_anchors():
-    """K beyond the wave's quarter of several chunks and 3.5% anchors."""
+@pytest.mark.parametrize("blocks", [1, 2, 4])
+def test_long_rows_and_many_anchors(blocks, tune):
+    """K of several windows of group sums, and 3.5% anchors."""
+    tune(qw.QW_TUNE_EXPERTS_ROW_BLOCKS, blocks)
     for fmt, n_out in (("2bit", 179), ("int4", 51), ("nf4", 0)):
         ex = Experts(fmt, 2, 48, 5120, n_out, seed=9)
         check(ex, 6, 1, "f16", seed=1)
