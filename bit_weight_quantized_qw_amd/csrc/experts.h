@@ -143,7 +143,13 @@ __device__ inline void fill_table(char *tab, const ExpertArgs &a) {
   }
 }
 
-// The products by tiles of 16 to 128 rows (experts_wide.hip).
+// The products by tiles of 32 or 64 rows (experts_wide.hip).
 qw_status launch_experts_wide(int fmt, int x_dtype, int row_blocks, const ExpertArgs &a, hipStream_t s);
+
+// The products by tiles of 128 or 256 rows (experts_tall.hip), and whether
+// that kernel takes the call: no anchors, not gated, Y of X's type or fp32,
+// and the rows and outputs within 32-bit offsets.
+bool experts_tall_fits(int x_dtype, const ExpertArgs &a);
+qw_status launch_experts_tall(int fmt, int x_dtype, int row_blocks, const ExpertArgs &a, hipStream_t s);
 
 }  // namespace qw

@@ -27,6 +27,8 @@
 // 4-bit codes); the matrix instruction wants eight per lane of 32
 // consecutive ones. A 4 x 4 transposition of dwords over the four lane
 // groups (two half-wave and two row swaps) turns one into the other.
+#include <math.h>
+
 #include "experts.h"
 
 namespace qw {
@@ -370,14 +372,51 @@ qw_status launch_fmt(int fmt, const ExpertArgs &a, hipStream_t s) {
   return launch_anch<QW_FMT_NF4_B64, DT>(a, s);
 }
 
-// 16-row blocks of a tile, from the mean number of rows of an expert.
-// 16 experts of 4096 x 2048 in 2-bit, us by the narrow kernel / tiles of 32
-// / of 64 rows: 8 rows an expert 27 / 37 / 46, 16: 40 / 39 / 48, 32: 58 / 49
-// / 66, 64: 100 / 78 / 68, 128: 177 / 117 / 100. Tiles of 128 rows leave
-// one wave a SIMD and were slower throughout (512 rows: 496 against 266).
-int row_blocks(int n, int G) {
-  const int mean = n / G;
-  return mean < 16 ? 1 : mean < 48 ? 2 : 4;
+// 16-row blocks of a tile: the kernel whose estimated time is least.
+//
+// A kernel's time is a start plus a share per 256 workgroups (one a CU),
+// the share (the narrow kernel's start too) growing with K; the tall tiles
+// go by whole rounds, each with its start. The rows per
+// expert are on the device, so the number of row tiles is estimated: the
+// rows by the tile's height and 0.6 of a short tile per expert, at least one
+// for every expert that can have a row. The constants are fits, in us at K =
+// 2048, to 16 experts of 4096 columns with 16 to 512 rows each, 64 of 2816
+// and 8 of 1024 to 14336; measured / estimated for 2-bit, us:
+//     rows an expert        narrow     32 rows     64 rows    128 rows
+//     16 x 4096:  16        39 / 45    38 / 47     48 / 59    38 / 33
+//                 64        98 / 101   77 / 78     68 / 75    62 / 66
+//                128       173 / 174  117 / 119   101 / 103   65 / 66
+//                512                  365 / 368   268 / 270  165 / 165
+//      8 x 1024:  32        23 / 40    62 / 65     81 / 87    56 / 56
+//    (K = 4096)  128        56 / 68    65 / 65     84 / 87    61 / 56
+//     8 x 14336 (K = 4096) 1024 rows: 64 rows 1615, 128 rows 965, 256 rows 933
+struct Cost {
+  float start, share;
+};
+int pick_row_blocks(int fmt, const ExpertArgs &a, bool tall) {
+  constexpr int kHeights[5] = {1, 2, 4, 8, 16};
+  constexpr Cost kCost[3][5] = {
+      {{12, 4.6f}, {24, 20.7f}, {31, 27.8f}, {10, 23}, {8, 50}},  // 2-bit
+      {{12, 6.1f}, {19, 17.6f}, {28, 25.2f}, {12, 31}, {8, 64}},  // NF4
+      {{12, 5.0f}, {21, 17.8f}, {27, 25.7f}, {12, 26}, {8, 56}},  // INT4
+  };
+  const Cost *cost = kCost[fmt == QW_FMT_2BIT_G32 ? 0 : fmt == QW_FMT_NF4_B64 ? 1 : 2];
+  double least = 1e30;
+  int best = 1;
+  for (int i = 0; i < (tall ? 5 : 3); ++i) {
+    const int h = 16 * kHeights[i];
+    const double tiles = fmax((double)a.n / h + 0.6 * a.G, fmin((double)a.n, (double)a.G));
+    const double cols = ceil((double)a.N / (i == 0 ? kCols : 256));
+    double rounds = fmax(fmin(tiles, (double)a.n) * cols / 256, i == 0 ? 0.0 : 1.0);
+    if (i >= 3) rounds = ceil(rounds);
+    const double k = a.K / 2048.0, share = cost[i].share * rounds * k;
+    const double t = i == 0 ? 4 + cost[i].start * k + share : cost[i].start * (i >= 3 ? rounds : 1.0) + share;
+    if (t < least) {
+      least = t;
+      best = kHeights[i];
+    }
+  }
+  return best;
 }
 
 // Argument checks the two entry points share; fills the weights' and rows'
@@ -416,9 +455,10 @@ qw_status check_experts(const qw_experts *ew, const void *X, qw_dtype x_dtype, c
 }
 
 qw_status run_experts(const qw_experts *ew, qw_dtype x_dtype, ExpertArgs &a, hipStream_t s) {
-  int blocks = row_blocks(a.n, a.G);
-  const int forced = tune(QW_TUNE_EXPERTS_ROW_BLOCKS);
-  if (forced >= 1) blocks = forced;
+  const bool tall = experts_tall_fits(x_dtype, a);
+  int blocks = tune(QW_TUNE_EXPERTS_ROW_BLOCKS);
+  if (blocks < 1) blocks = pick_row_blocks(ew->w.format, a, tall);
+  if (blocks > 4 && tall) return launch_experts_tall(ew->w.format, x_dtype, blocks, a, s);
   if (blocks > 1) return launch_experts_wide(ew->w.format, x_dtype, blocks, a, s);
   const int cols = a.swiglu ? kCols / 2 : kCols;
   a.col_tiles = (a.out_n + cols - 1) / cols;

@@ -602,10 +602,12 @@ typedef struct {
  *      is 0); g->G == ew->E
  *   Y  device [g->n][N or I] of y_dtype F16, BF16 or F32, rounded once;
  *      rows of positions in no group are left as they were.
- * fp32 accumulation. The weights' scales multiply fp32 sums of code levels,
- * so no weight is rounded to x_dtype; the NF4 levels are, to two numbers of
- * it (n < 16 E) or to one after a common factor (n >= 16 E: at most half a
- * step off, a third of that in the mean). K must be a multiple of 64
+ * fp32 accumulation. Gated products, experts with anchors, and any with
+ * few rows per expert scale fp32 sums of exact code levels, so no weight is
+ * rounded (NF4 levels are, to two numbers of x_dtype, or with more rows to
+ * one after a common factor); plain products with more rows round the
+ * weights to x_dtype, as qgemm_prefill does (F16: infinite beyond 65504).
+ * K must be a multiple of 64
  * and N K below 2^32. No workspace.
  * Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED, HIP. */
 qw_status qgemm_experts(const qw_experts *ew, const void *X, qw_dtype x_dtype,

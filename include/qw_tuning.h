@@ -42,7 +42,8 @@ typedef enum {
    * shape, 1 the vector-ALU kernel. */
   QW_TUNE_INT4_PATH = 6,
   /* Experts' products: -1 / 0 automatic, 1 the narrow kernel (16 rows), 2 or
-   * 4 the wide one with tiles of that many 16-row blocks. */
+   * 4 the wide one with tiles of that many 16-row blocks, 8 or 16 the tall
+   * one where it takes the call (else 4). */
   QW_TUNE_EXPERTS_ROW_BLOCKS = 7
 } qw_tune_key;
 

@@ -78,9 +78,9 @@ def device_groups(ids, G):
     return qw.RowGroups(to_dev(off), to_dev(rows)), off, rows
 
 
-def products(ex, x64, off, wide, dtype):
+def products(ex, x64, off, wide, dtype, tall=False):
     """(values, bounds) of the rows in grouped order: row p times its group's
-    weights; wide: by the kernel of wide tiles."""
+    weights; wide, tall: by the kernels of wide and of tall tiles."""
     y = np.zeros((x64.shape[0], ex.N))
     tol = np.zeros_like(y)
     extra = 0.0
@@ -88,6 +88,8 @@ def products(ex, x64, off, wide, dtype):
         extra = half_step(dtype) if wide else half_step(dtype) ** 2
     elif ex.fmt == "2bit" and wide:  # Z and the group sums of x as two bf16 numbers, without the product of the rests
         extra = 2.0 ** -15
+    if tall:  # every weight is rounded to dtype (and to fp32 before)
+        extra = half_step(dtype) + F32
     for e in range(ex.E):
         s = slice(off[e], off[e + 1])
         y[s] = x64[s] @ ex.W[e].T

@@ -13,9 +13,19 @@ pytestmark = pytest.mark.gpu
 
 
 def is_wide(n, E):
-    """Whether the call takes the kernel of wide tiles."""
+    """Whether the call may take the kernel of wide tiles (by itself it
+    chooses by an estimate of the time, from several rows an expert on)."""
     forced = qw.qw_tune_get(qw.QW_TUNE_EXPERTS_ROW_BLOCKS)
-    return forced > 1 if forced > 0 else n // E >= 16
+    return forced > 1 if forced > 0 else n > 2 * E
+
+
+def is_tall(n, ex, dt, odt, swiglu):
+    """Whether it may take the kernel of tall tiles, whose weights are
+    rounded to the activations' type."""
+    import torch
+    forced = qw.qw_tune_get(qw.QW_TUNE_EXPERTS_ROW_BLOCKS)
+    fits = odt in (dt, torch.float32) and not swiglu and not ex.packed[0].n_out
+    return fits and (forced >= 8 if forced > 0 else n > 8 * ex.E)
 
 
 def acts(rng, rows, K, dt):
@@ -45,7 +55,8 @@ def check(ex, T, k, dtype, out="f32", swiglu=False, seed=0, none=0.1, grouped=Fa
     got = qw.qgemm_experts(ex.ew, x, g, top_k=None if grouped else k, swiglu=swiglu, out=Y)
     assert got is Y
     x64 = x.double().cpu().numpy()
-    y, tol = products(ex, x64 if grouped else x64[rows // k], off, is_wide(T * k, ex.E), dt)
+    y, tol = products(ex, x64 if grouped else x64[rows // k], off, is_wide(T * k, ex.E), dt,
+                      is_tall(T * k, ex, dt, odt, swiglu))
     if swiglu:
         y, tol = gated(y, tol)
     m = off[-1]
@@ -71,7 +82,7 @@ def test_few_rows(fmt, n_out, dtype, N, K):
 @pytest.mark.parametrize("fmt,n_out", FORMATS)
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
 @pytest.mark.parametrize("N,K", [(40, 192), (260, 448), (300, 1024)])
-@pytest.mark.parametrize("blocks", [None, 1, 2, 4])
+@pytest.mark.parametrize("blocks", [None, 1, 2, 4, 8, 16])
 def test_many_rows(fmt, n_out, dtype, N, K, blocks, tune):
     """Some hundred rows an expert, unevenly, by every tile height."""
     if blocks:
@@ -85,7 +96,7 @@ def test_many_rows(fmt, n_out, dtype, N, K, blocks, tune):
 @pytest.mark.parametrize("fmt,n_out", FORMATS)
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
 @pytest.mark.parametrize("T,k", [(1, 2), (9, 3), (200, 3)])
-@pytest.mark.parametrize("blocks", [None, 1, 2, 4])
+@pytest.mark.parametrize("blocks", [None, 1, 2, 4, 8, 16])
 def test_gated(fmt, n_out, dtype, T, k, blocks, tune):
     if blocks:
         tune(qw.QW_TUNE_EXPERTS_ROW_BLOCKS, blocks)
@@ -103,7 +114,7 @@ def test_grouped_input_and_other_output_types(fmt, n_out, T, k):
     check(ex, T, k, "bf16", out="f16", seed=2, grouped=True)
 
 
-@pytest.mark.parametrize("blocks", [1, 2, 4])
+@pytest.mark.parametrize("blocks", [1, 2, 4, 8, 16])
 def test_long_rows_and_many_anchors(blocks, tune):
     """K of several windows of group sums, and 3.5% anchors."""
     tune(qw.QW_TUNE_EXPERTS_ROW_BLOCKS, blocks)
@@ -130,10 +141,12 @@ def test_all_rows_one_expert_and_none():
             assert_close(Y, y, tol, torch.float32)
 
 
-def test_infinite_and_nan_rows_stay_in_their_rows():
+@pytest.mark.parametrize("blocks", [1, 2, 4, 8, 16])
+def test_infinite_and_nan_rows_stay_in_their_rows(blocks, tune):
     """A row's infinities and NaN reach no other row, and none of an anchor
     channel's reach the columns' coded part."""
     import torch
+    tune(qw.QW_TUNE_EXPERTS_ROW_BLOCKS, blocks)
     for fmt, n_out in FORMATS:
         ex = Experts(fmt, 2, 96, 256, n_out, seed=6)
         for n in (7, 150):
@@ -151,19 +164,21 @@ def test_infinite_and_nan_rows_stay_in_their_rows():
             assert not bool(torch.isfinite(Y[n // 2]).any())
 
 
-def test_offsets_that_do_not_fit_stay_in_bounds():
+@pytest.mark.parametrize("blocks", [1, 2, 4, 8, 16])
+def test_offsets_that_do_not_fit_stay_in_bounds(blocks, tune):
     """Offsets beyond the rows, descending or negative, and rows out of range:
     the rows that can be are computed, nothing else is touched."""
     import torch
+    tune(qw.QW_TUNE_EXPERTS_ROW_BLOCKS, blocks)
     ex = Experts("nf4", 3, 40, 128, 0, seed=8)
     n = 20
-    x = acts(np.random.default_rng(0), n, 128, torch.float16)
+    x = acts(np.random.default_rng(0), n, 128, torch.bfloat16)
     for off in ([0, 5, 400, 500], [-7, 3, 2, 20], [0, 0, 0, 0], [20, 20, 20, 20]):
         rows = np.arange(n, dtype=np.int32)
         rows[4] = 10**6
         rows[5] = -3
         g = qw.RowGroups(to_dev(np.array(off, np.int32)), to_dev(rows))
-        guard = torch.full((n + 64, 40), 5.0, device="cuda")
+        guard = torch.full((n + 64, 40), 5.0, dtype=torch.bfloat16, device="cuda")
         qw.qgemm_experts(ex.ew, x, g, out=guard[:n])
         torch.cuda.synchronize()
         assert bool((guard[n:] == 5.0).all())
@@ -183,7 +198,7 @@ def test_combine(fmt, n_out, T, k, N, dtype):
     w[ids < 0] = np.nan  # what an empty slot holds does not matter
     g, off, rows = device_groups(ids, E)
     h = acts(rng, T * k, K, dt)
-    y, tol = products(ex, h.double().cpu().numpy(), off, is_wide(T * k, E), dt)
+    y, tol = products(ex, h.double().cpu().numpy(), off, is_wide(T * k, E), dt, is_tall(T * k, ex, dt, torch.float32, False))
     slot_y, slot_t = np.zeros((T * k, N)), np.zeros((T * k, N))
     slot_y[rows[: off[-1]]] = y[: off[-1]]
     slot_t[rows[: off[-1]]] = tol[: off[-1]]
