@@ -110,14 +110,41 @@ __device__ inline TileAt place_tile(const int32_t *offsets, int G, int n, int he
   return TileAt{find_row_tile(offsets, G, n, height, band * 8 + w % high), w / high};
 }
 
+// INT4 operands without a table: a nibble u put into the top mantissa bits
+// of 16 is the number 16 + u, and two nibbles 16 bits apart are done at
+// once. The elements of a word then come in the order 0 4 1 5 2 6 3 7, which
+// the operand of X is brought into, and the products start from -24 times
+// the row sums of x.
+template <int DT>
+struct Int4 {
+  static constexpr int kAt = DT == QW_DT_F16 ? 6 : 3;  // where the top four mantissa bits begin
+  static constexpr uint32_t kSixteen = (DT == QW_DT_F16 ? 0x4C00u : 0x4180u) * 0x10001u;
+  static constexpr uint32_t kMinus24 = (DT == QW_DT_F16 ? 0xCE00u : 0xC1C0u) * 0x10001u;
+  static __device__ u32x4 operand(uint32_t c, uint32_t sixteen) {
+    constexpr uint32_t mask = 0x000F000Fu << kAt;
+    u32x4 b;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int up = kAt - 4 * q;
+      b[q] = ((up >= 0 ? c << (up & 31) : c >> (-up & 31)) & mask) | sixteen;
+    }
+    return b;
+  }
+  static __device__ u32x4 order(u32x4 x) {
+    return u32x4{__builtin_amdgcn_perm(x[2], x[0], 0x05040100u), __builtin_amdgcn_perm(x[2], x[0], 0x07060302u),
+                 __builtin_amdgcn_perm(x[3], x[1], 0x05040100u), __builtin_amdgcn_perm(x[3], x[1], 0x07060302u)};
+  }
+};
+
 // Level table: entry of code byte v, replica r. 2-bit: four levels (8
-// bytes), INT4 and wide NF4: two (4 bytes, two replicas side by side),
-// narrow NF4: the nearest two and the rests of both (8 bytes).
+// bytes), wide NF4: two (4 bytes, two replicas side by side), narrow NF4:
+// the nearest two and the rests of both (8 bytes).
 constexpr int kEntry = 128;  // bytes of one byte's replicas
 template <int FMT, int DT, int kThreads, bool WIDE = false>
 __device__ inline void fill_table(char *tab, const ExpertArgs &a) {
-  for (int i = threadIdx.x; i < 256 * 8; i += kThreads) {
-    const int v = i >> 3;
+  // one entry's value per thread, then its 128 bytes; neighbours start at
+  // different pieces, so that they write different banks
+  for (int v = threadIdx.x; v < 256; v += kThreads) {
     u32x2 w;
     if (FMT == QW_FMT_2BIT_G32) {
       uint32_t l[4];
@@ -127,9 +154,6 @@ __device__ inline void fill_table(char *tab, const ExpertArgs &a) {
         l[t] = Op<DT>::bits(q == 0 ? -152.0f : q == 1 ? -45.0f : q == 2 ? 45.0f : 152.0f);
       }
       w = u32x2{l[0] | (l[1] << 16), l[2] | (l[3] << 16)};
-    } else if (FMT == QW_FMT_INT4_G32) {
-      const uint32_t p = Op<DT>::bits((float)((v & 15) - 8)) | (Op<DT>::bits((float)((v >> 4) - 8)) << 16);
-      w = u32x2{p, p};
     } else if (WIDE) {
       const uint32_t p = Op<DT>::bits(a.nf4[v & 15]) | (Op<DT>::bits(a.nf4[v >> 4]) << 16);
       w = u32x2{p, p};
@@ -139,7 +163,9 @@ __device__ inline void fill_table(char *tab, const ExpertArgs &a) {
       w = u32x2{lo16 | (hi16 << 16),
                 Op<DT>::bits(lo - Op<DT>::value(lo16)) | (Op<DT>::bits(hi - Op<DT>::value(hi16)) << 16)};
     }
-    *reinterpret_cast<u32x4 *>(tab + v * kEntry + (i & 7) * 16) = u32x4{w[0], w[1], w[0], w[1]};
+#pragma unroll
+    for (int r = 0; r < 8; ++r)
+      *reinterpret_cast<u32x4 *>(tab + v * kEntry + ((r + v) & 7) * 16) = u32x4{w[0], w[1], w[0], w[1]};
   }
 }
 

@@ -29,6 +29,8 @@
 // groups (two half-wave and two row swaps) turns one into the other.
 #include <math.h>
 
+#include <type_traits>
+
 #include "experts.h"
 
 namespace qw {
@@ -52,27 +54,29 @@ struct Chunk {
 };
 
 template <int FMT, int DT, bool ANCH>
-__global__ __launch_bounds__(kThreads) void experts_kernel(ExpertArgs a) {
+__global__ __launch_bounds__(kThreads, 3) void experts_kernel(ExpertArgs a) {
   using O = Op<DT>;
-  __shared__ __attribute__((aligned(16))) char tab[256 * kEntry];
-  __shared__ __attribute__((aligned(16))) float part[kWaves][kRows][kCols + 4];
+  // the level table; behind the loop the waves' sums lie there
+  constexpr bool k4 = FMT == QW_FMT_INT4_G32;
+  constexpr int kSums = kWaves * kRows * (kCols + 4) * 4, kTable = k4 ? 0 : 256 * kEntry;
+  __shared__ __attribute__((aligned(16))) char tab[kTable > kSums ? kTable : kSums];
+  float(*const part)[kRows][kCols + 4] = reinterpret_cast<float(*)[kRows][kCols + 4]>(tab);
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int ln = lane & 15, lg = lane >> 4;
   const int tile = blockIdx.x / a.col_tiles, ct = blockIdx.x % a.col_tiles;
+  const RowLookup row_at(a.rows, a.n);
   const RowTile rt = find_row_tile(a.offsets, a.G, a.n, kRows, tile);
   if (rt.cnt == 0) return;
   const int e = rt.g, K = a.K;
 
-  fill_table<FMT, DT, kThreads>(tab, a);
-
   // this lane's row of A: rows past the tile's end repeat its first row
   // (their products are not stored)
-  const int p = rt.p0 + (ln < rt.cnt ? ln : 0);
-  int xr = a.x_div ? a.rows[p] / a.x_div : p;
-  if ((uint32_t)xr >= (uint32_t)a.x_rows) xr = 0;
-  const uint16_t *const xp = a.X + (size_t)xr * K;
+  const bool few = rt.cnt <= 4;
+  const int lr = few ? ln & 3 : ln;
+  const int p = rt.p0 + (lr < rt.cnt ? lr : 0);
+  int xr = a.x_div ? row_at(p) : p;
 
   // columns: gated tiles take 32 gate columns and the same 32 up columns
   const int half_cols = a.swiglu ? kCols / 2 : kCols;
@@ -116,7 +120,19 @@ __global__ __launch_bounds__(kThreads) void experts_kernel(ExpertArgs a) {
         const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(rc, (int)(oc == kOob ? kOob : oc + 4 * i), 0, 0);
         d.c[j][i] = v[0]; d.c[j][i + 1] = v[1]; d.c[j][i + 2] = v[2]; d.c[j][i + 3] = v[3];
       }
-      if (CH::kScales == 2) {
+      if (few && FMT != QW_FMT_NF4_B64) {  // those of groups lg and 4 + lg of the chunk
+        constexpr uint32_t kWord = FMT == QW_FMT_2BIT_G32 ? 4 : 2;
+        const int g = ch * (kChunk / 32) + lg;
+        const uint32_t o0 = wn[j] >= 0 && g < K / 32 ? so[j] + (uint32_t)g * kWord : kOob;
+        const uint32_t o1 = wn[j] >= 0 && g + 4 < K / 32 ? so[j] + (uint32_t)(g + 4) * kWord : kOob;
+        if (FMT == QW_FMT_2BIT_G32) {
+          d.s[j][0] = __builtin_amdgcn_raw_buffer_load_b32(rs, (int)o0, 0, 0);
+          d.s[j][CH::kScales - 1] = __builtin_amdgcn_raw_buffer_load_b32(rs, (int)o1, 0, 0);
+        } else {
+          d.s[j][0] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(rs, (int)o0, 0, 0) |
+                      (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(rs, (int)o1, 0, 0) << 16;
+        }
+      } else if (CH::kScales == 2) {
         const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(rs, (int)os, 0, 0);
         d.s[j][0] = v[0];
         d.s[j][CH::kScales - 1] = v[1];
@@ -126,101 +142,210 @@ __global__ __launch_bounds__(kThreads) void experts_kernel(ExpertArgs a) {
     }
   };
 
+  const uint16_t *xp = a.X;  // this lane's row, once its number is there
   f32x4 acc[kSub];
 #pragma unroll
   for (int j = 0; j < kSub; ++j) acc[j] = f32x4{0, 0, 0, 0};
   const f32x4 zero = {0, 0, 0, 0};
-  const uint32_t rep = FMT == QW_FMT_INT4_G32 ? (uint32_t)(lane & 31) * 4u : (uint32_t)(lane & 15) * 8u;
+  const uint32_t rep = (uint32_t)(lane & 15) * 8u;
+  uint32_t sixteen = Int4<DT>::kSixteen;
+  if (k4) asm volatile("" : "+v"(sixteen));  // an and-or takes one scalar operand
   auto entry = [&](uint32_t byte) { return tab + ((byte << 7) | rep); };
+  // 64 elements of X from k on: this lane's eight of each 32
+  auto load_x = [&](int k, u32x4 (&d)[2]) {
+    d[0] = *reinterpret_cast<const u32x4 *>(xp + k + lg * 8);
+    d[1] = *reinterpret_cast<const u32x4 *>(xp + k + 32 + lg * 8);
+  };
 
-  // products of the eight 32-weight steps of a chunk
-  auto multiply = [&](int ch, CH &d) {
-    const int k0 = ch * kChunk;
-    const int steps = min(8, (K - k0) / 32);
+  // Operand of column block j for step h (32 weights) of run s of a chunk.
+  struct Operand {
+    u32x4 b, rest;  // NF4: the levels' second parts
+  };
+  auto operand = [&](const uint32_t (&c)[kSub][CH::kCodes], int j, int s, int h) {
+    Operand o;
+    if (FMT == QW_FMT_2BIT_G32) {
+      const uint32_t w = c[j][s] >> (16 * h);
+      const u32x2 lo = *reinterpret_cast<const u32x2 *>(entry(w & 0xFFu));
+      const u32x2 hi = *reinterpret_cast<const u32x2 *>(entry((w >> 8) & 0xFFu));
+      o.b = u32x4{lo[0], lo[1], hi[0], hi[1]};
+    } else if (k4) {
+      o.b = Int4<DT>::operand(c[j][(4 * h + s) % CH::kCodes], sixteen);
+    } else {
+      const uint32_t w = c[j][(4 * h + s) % CH::kCodes];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const u32x2 l = *reinterpret_cast<const u32x2 *>(entry((w >> (8 * q)) & 0xFFu));
+        o.b[q] = l[0];
+        o.rest[q] = l[1];
+      }
+    }
+    return o;
+  };
+  // Operand of X for the 32 elements from k on, and what goes with it: 100
+  // times its row sums (2-bit, for Z) or -24 times them (INT4: the products
+  // start there, so that 16 + u counts as u - 8).
+  auto prepare = [&](int k, u32x4 A, u32x4 &x_op, const f32x4 &from, f32x4 &sums) {
+    if (FMT == QW_FMT_2BIT_G32) {
+      if (ANCH) {
+        const uint32_t m = a.mask[(size_t)e * (K / 32) + k / 32] >> (8 * lg);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          A[q] &= ~(((m >> (2 * q)) & 1 ? 0xFFFFu : 0u) | ((m >> (2 * q + 1)) & 1 ? 0xFFFF0000u : 0u));
+      }
+      const uint32_t hundred = Op<DT>::bits(100.0f) * 0x10001u;
+      sums = O::mma(A, u32x4{hundred, hundred, hundred, hundred}, from);
+    }
+    if (k4) {
+      A = Int4<DT>::order(A);
+      constexpr uint32_t m = Int4<DT>::kMinus24;
+      sums = O::mma(A, u32x4{m, m, m, m}, from);
+    }
+    x_op = A;
+  };
+  // to += the products D (and sums) by the scale word w
+  auto scale_in = [&](f32x4 &to, uint32_t w, const f32x4 &D, const f32x4 &sums) {
+    const float S = FMT == QW_FMT_NF4_B64 ? __builtin_bit_cast(float, w) : f16_bits_to_f32((uint16_t)w);
+    const float Z = f16_bits_to_f32((uint16_t)(w >> 16));
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      to[r] = __builtin_fmaf(S, D[r], FMT == QW_FMT_2BIT_G32 ? __builtin_fmaf(Z, sums[r], to[r]) : to[r]);
+  };
+
+  // the table while the first codes and the rows' numbers are on their way
+  auto table_and_rows = [&] {
+    if (!k4) {
+      fill_table<FMT, DT, kThreads>(tab, a);
+      __syncthreads();
+    }
+    if (a.x_div) xr /= a.x_div;
+    if ((uint32_t)xr >= (uint32_t)a.x_rows) xr = 0;
+    xp = a.X + (size_t)xr * K;
+  };
+
+  // The loops over chunks stay rolled: a short launch spends much of its time
+  // fetching instructions.
+  if (few) {
+    // Up to four rows: operand row 4 s + m is row m of X in the s-th of four
+    // consecutive scale groups and zero in the others, so four products run
+    // into one result, whose rows lane group s holds for its own group: one
+    // scaling per four products, by a scale word that only that lane group
+    // needs. The groups' sums are added up with the waves'.
+    constexpr int kGroup = FMT == QW_FMT_NF4_B64 ? 64 : 32, kQuads = kChunk / (4 * kGroup);
+    const int slot = ln >> 2;
+    auto load_xf = [&](int ch, u32x4 (&v)[2]) {  // the lane's own groups, 16 bytes each
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int k = FMT == QW_FMT_NF4_B64 ? ch * kChunk + slot * 64 + q * 32 : ch * kChunk + (q * 4 + slot) * 32;
+        v[q] = *reinterpret_cast<const u32x4 *>(xp + (k < K ? k + lg * 8 : 0));
+        if (k >= K) v[q] = u32x4{0, 0, 0, 0};
+      }
+    };
+    CH next;
+    u32x4 xn[2];
+    if (ch0 < ch1) load(ch0, next);
+    table_and_rows();
+    if (ch0 < ch1) load_xf(ch0, xn);
+#pragma unroll 1
+    for (int ch = ch0; ch < ch1; ++ch) {
+      CH d = next;
+      u32x4 x[2] = {xn[0], xn[1]};
+      if (ch + 1 < ch1) {
+        load(ch + 1, next);
+        load_xf(ch + 1, xn);
+      }
+#pragma unroll
+      for (int j = 0; j < kSub; ++j) {
+        if (FMT == QW_FMT_2BIT_G32) to_halves(reinterpret_cast<uint32_t(&)[4]>(d.c[j][0]));
+#pragma unroll
+        for (int i = 0; i < CH::kCodes; i += 4) transpose4(reinterpret_cast<uint32_t(&)[4]>(d.c[j][i]));
+      }
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        if (FMT == QW_FMT_2BIT_G32 && ANCH) {
+          const int g = ch * (kChunk / 32) + q * 4 + slot;
+          const uint32_t m = g < K / 32 ? a.mask[(size_t)e * (K / 32) + g] >> (8 * lg) : 0u;
+#pragma unroll
+          for (int t = 0; t < 4; ++t)
+            x[q][t] &= ~(((m >> (2 * t)) & 1 ? 0xFFFFu : 0u) | ((m >> (2 * t + 1)) & 1 ? 0xFFFF0000u : 0u));
+        }
+        if (k4) x[q] = Int4<DT>::order(x[q]);
+      }
+#pragma unroll
+      for (int q = 0; q < kQuads; ++q) {
+        f32x4 sums = zero, D[kSub];
+#pragma unroll
+        for (int j = 0; j < kSub; ++j) D[j] = zero;
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+#pragma unroll
+          for (int h = 0; h < (kQuads == 1 ? 2 : 1); ++h) {
+            u32x4 A = kQuads == 1 ? x[h] : x[q];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) A[t] = slot == s ? A[t] : 0u;
+            constexpr uint32_t m24 = Int4<DT>::kMinus24;
+            const uint32_t hundred = Op<DT>::bits(100.0f) * 0x10001u, ones = k4 ? m24 : hundred;
+            if (kQuads != 1) sums = O::mma(A, u32x4{ones, ones, ones, ones}, sums);
+            // step (32 weights) 4 q + s of the chunk; NF4: 2 s + h
+            const int step = kQuads == 1 ? 2 * s + h : 4 * q + s;
+#pragma unroll
+            for (int j = 0; j < kSub; ++j) {
+              const Operand w = operand(d.c, j, step >> 1, step & 1);
+              D[j] = O::mma(A, w.b, D[j]);
+              if (FMT == QW_FMT_NF4_B64) D[j] = O::mma(A, w.rest, D[j]);
+            }
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < kSub; ++j) {
+          if (k4) D[j] += sums;
+          scale_in(acc[j], k4 ? d.s[j][0] >> (16 * q) : d.s[j][q % CH::kScales], D[j], sums);
+        }
+      }
+    }
+  } else {
+  CH next;
+  u32x4 x[4][2];
+  const int k_end = min(ch1 * kChunk, K);
+  if (ch0 < ch1) load(ch0, next);
+  table_and_rows();
+  if (ch0 < ch1) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) load_x(min(ch0 * kChunk + 64 * i, k_end - 64), x[i]);
+  }
+#pragma unroll 1
+  for (int ch = ch0; ch < ch1; ++ch) {
+    CH d = next;
+    if (ch + 1 < ch1) load(ch + 1, next);
+    uint32_t sc[kSub][CH::kScales][4];
 #pragma unroll
     for (int j = 0; j < kSub; ++j) {
       if (FMT == QW_FMT_2BIT_G32) to_halves(reinterpret_cast<uint32_t(&)[4]>(d.c[j][0]));
 #pragma unroll
-      for (int i = 0; i < CH::kCodes; i += 4)
-        transpose4(reinterpret_cast<uint32_t(&)[4]>(d.c[j][i]));
-    }
-    uint32_t sc[kSub][CH::kScales][4];
-#pragma unroll
-    for (int j = 0; j < kSub; ++j)
+      for (int i = 0; i < CH::kCodes; i += 4) transpose4(reinterpret_cast<uint32_t(&)[4]>(d.c[j][i]));
 #pragma unroll
       for (int i = 0; i < CH::kScales; ++i) gather4(d.s[j][i], sc[j][i]);
-
+    }
+    const int k0 = ch * kChunk;
 #pragma unroll
-    for (int t = 0; t < 8; ++t) {
-      if (t < steps) {
-        u32x4 A = *reinterpret_cast<const u32x4 *>(xp + k0 + t * 32 + lg * 8);
-        const int src = t >> 1, h = t & 1;  // source lane group and half of its run
-        f32x4 xs = zero;
-        if (FMT == QW_FMT_2BIT_G32) {
-          if (ANCH) {
-            const uint32_t m = a.mask[(size_t)e * (K / 32) + (k0 / 32 + t)] >> (8 * lg);
+    for (int i = 0; i < 4; ++i) {
+      const int k = k0 + 64 * i;
+      if (k >= K) break;  // uniform
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const uint32_t drop = ((m >> (2 * q)) & 1 ? 0xFFFFu : 0u) | ((m >> (2 * q + 1)) & 1 ? 0xFFFF0000u : 0u);
-              A[q] &= ~drop;
-            }
-          }
-          const uint32_t hundred = Op<DT>::bits(100.0f) * 0x10001u;
-          xs = O::mma(A, u32x4{hundred, hundred, hundred, hundred}, zero);
-        }
+      for (int h = 0; h < 2; ++h) {
+        u32x4 xo;
+        f32x4 sums = zero;
+        prepare(k + 32 * h, x[i][h], xo, sums, sums);
 #pragma unroll
         for (int j = 0; j < kSub; ++j) {
-          u32x4 B, B2;
-          if (FMT == QW_FMT_2BIT_G32) {
-            const uint32_t c = d.c[j][src] >> (16 * h);
-            const u32x2 lo = *reinterpret_cast<const u32x2 *>(entry(c & 0xFFu));
-            const u32x2 hi = *reinterpret_cast<const u32x2 *>(entry((c >> 8) & 0xFFu));
-            B = u32x4{lo[0], lo[1], hi[0], hi[1]};
-          } else {
-            const uint32_t c = d.c[j][(4 * h + src) % CH::kCodes];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const char *en = entry((c >> (8 * q)) & 0xFFu);
-              if (FMT == QW_FMT_INT4_G32) {
-                B[q] = *reinterpret_cast<const uint32_t *>(en);
-              } else {
-                const u32x2 w = *reinterpret_cast<const u32x2 *>(en);
-                B[q] = w[0];
-                B2[q] = w[1];
-              }
-            }
-          }
-          f32x4 D = O::mma(A, B, zero);
-          if (FMT == QW_FMT_NF4_B64) {
-            D = O::mma(A, B2, D);
-            const float am = __builtin_bit_cast(float, sc[j][0][src]);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) acc[j][r] = __builtin_fmaf(am, D[r], acc[j][r]);
-          } else if (FMT == QW_FMT_INT4_G32) {
-            const float s = f16_bits_to_f32((uint16_t)(sc[j][0][src] >> (16 * h)));
-#pragma unroll
-            for (int r = 0; r < 4; ++r) acc[j][r] = __builtin_fmaf(s, D[r], acc[j][r]);
-          } else {
-            const uint32_t w = sc[j][h % CH::kScales][src];
-            const float S = f16_bits_to_f32((uint16_t)w), Z = f16_bits_to_f32((uint16_t)(w >> 16));
-#pragma unroll
-            for (int r = 0; r < 4; ++r) acc[j][r] = __builtin_fmaf(S, D[r], __builtin_fmaf(Z, xs[r], acc[j][r]));
-          }
+          const Operand w = operand(d.c, j, i, h);
+          f32x4 D = O::mma(xo, w.b, k4 ? sums : zero);
+          if (FMT == QW_FMT_NF4_B64) D = O::mma(xo, w.rest, D);
+          scale_in(acc[j], FMT == QW_FMT_NF4_B64 || k4 ? sc[j][0][i] >> (k4 ? 16 * h : 0) : sc[j][h % CH::kScales][i], D, sums);
         }
       }
+      load_x(min(k + kChunk, k_end - 64), x[i]);
     }
-  };
-
-  CH buf[2];
-  if (ch0 < ch1) load(ch0, buf[0]);
-  __syncthreads();  // the level table
-  for (int ch = ch0; ch < ch1; ch += 2) {
-    if (ch + 1 < ch1) load(ch + 1, buf[1]);
-    multiply(ch, buf[0]);
-    if (ch + 1 < ch1) {
-      if (ch + 2 < ch1) load(ch + 2, buf[0]);
-      multiply(ch + 1, buf[1]);
-    }
+  }
   }
   if (FMT == QW_FMT_2BIT_G32) {
 #pragma unroll
@@ -228,14 +353,15 @@ __global__ __launch_bounds__(kThreads) void experts_kernel(ExpertArgs a) {
   }
 
   if (ANCH) {
-    // the anchor channels: 32 of them a step, the waves in turn. bf16
-    // operands take the fp16 anchor as two parts.
-    for (int o0 = wv * 32; o0 < a.n_out; o0 += kWaves * 32) {
+    // the anchor channels: 32 of them a step, the waves in turn from the
+    // last, which has the fewest chunks. bf16 operands take the fp16 anchor
+    // as two parts.
+    for (int o0 = (kWaves - 1 - wv) * 32; o0 < a.n_out; o0 += kWaves * 32) {
       const int o = o0 + lg * 8;
       u32x4 A = {0, 0, 0, 0};
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
-        if (o + q < a.n_out) {
+        if (o + q < a.n_out && (!few || ln < 4)) {  // few: in the rows of the first group
           int k = o + q;
           if (FMT == QW_FMT_2BIT_G32) {
             k = a.idx[(size_t)e * a.n_out + o + q];
@@ -257,7 +383,8 @@ __global__ __launch_bounds__(kThreads) void experts_kernel(ExpertArgs a) {
     }
   }
 
-  // ---- the four waves' sums, then one rounding ----
+  // ---- the waves' sums, then one rounding ----
+  __syncthreads();  // the table is done with
 #pragma unroll
   for (int j = 0; j < kSub; ++j)
 #pragma unroll
@@ -273,8 +400,17 @@ __global__ __launch_bounds__(kThreads) void experts_kernel(ExpertArgs a) {
     return;
   }
   auto total = [&](int c) {
-    return *reinterpret_cast<const f32x4 *>(&part[0][row][c]) + *reinterpret_cast<const f32x4 *>(&part[1][row][c]) +
-           *reinterpret_cast<const f32x4 *>(&part[2][row][c]) + *reinterpret_cast<const f32x4 *>(&part[3][row][c]);
+    f32x4 v = {0, 0, 0, 0};
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      if (few) {
+#pragma unroll
+        for (int g = 0; g < 4; ++g) v += *reinterpret_cast<const f32x4 *>(&part[w][4 * g + row][c]);
+      } else {
+        v += *reinterpret_cast<const f32x4 *>(&part[w][row][c]);
+      }
+    }
+    return v;
   };
   const int c = (tid & 15) * 4;
   if (c >= half_cols) return;
@@ -383,12 +519,12 @@ qw_status launch_fmt(int fmt, const ExpertArgs &a, hipStream_t s) {
 // 2048, to 16 experts of 4096 columns with 16 to 512 rows each, 64 of 2816
 // and 8 of 1024 to 14336; measured / estimated for 2-bit, us:
 //     rows an expert        narrow     32 rows     64 rows    128 rows
-//     16 x 4096:  16        39 / 45    38 / 47     48 / 59    38 / 33
-//                 64        98 / 101   77 / 78     68 / 75    62 / 66
-//                128       173 / 174  117 / 119   101 / 103   65 / 66
+//     16 x 4096:  16        35 / 37    36 / 47     46 / 59    38 / 33
+//                 64        98 / 93    77 / 78     68 / 75    62 / 66
+//                128       173 / 166  117 / 119   101 / 103   65 / 66
 //                512                  365 / 368   268 / 270  165 / 165
-//      8 x 1024:  32        23 / 40    62 / 65     81 / 87    56 / 56
-//    (K = 4096)  128        56 / 68    65 / 65     84 / 87    61 / 56
+//      8 x 1024:  32        22 / 24    60 / 65     80 / 87    56 / 56
+//    (K = 4096)  128        56 / 52    65 / 65     84 / 87    61 / 56
 //     8 x 14336 (K = 4096) 1024 rows: 64 rows 1615, 128 rows 965, 256 rows 933
 struct Cost {
   float start, share;
@@ -396,9 +532,9 @@ struct Cost {
 int pick_row_blocks(int fmt, const ExpertArgs &a, bool tall) {
   constexpr int kHeights[5] = {1, 2, 4, 8, 16};
   constexpr Cost kCost[3][5] = {
-      {{12, 4.6f}, {24, 20.7f}, {31, 27.8f}, {10, 23}, {8, 50}},  // 2-bit
-      {{12, 6.1f}, {19, 17.6f}, {28, 25.2f}, {12, 31}, {8, 64}},  // NF4
-      {{12, 5.0f}, {21, 17.8f}, {27, 25.7f}, {12, 26}, {8, 56}},  // INT4
+      {{4, 4.6f}, {24, 20.7f}, {31, 27.8f}, {10, 23}, {8, 50}},  // 2-bit
+      {{4, 5.0f}, {23, 17.6f}, {28, 25.2f}, {12, 31}, {8, 64}},  // NF4
+      {{6, 5.2f}, {21, 17.8f}, {27, 25.7f}, {12, 26}, {8, 56}},  // INT4
   };
   const Cost *cost = kCost[fmt == QW_FMT_2BIT_G32 ? 0 : fmt == QW_FMT_NF4_B64 ? 1 : 2];
   double least = 1e30;

@@ -40,7 +40,7 @@ constexpr int kSumLd = 36;    // floats per row of a window of 32 group sums
 template <int FMT, int DT, bool ANCH, int MR>
 __global__ __launch_bounds__(kThreads, 2) void wide_kernel(ExpertArgs a) {
   using O = Op<DT>;
-  constexpr bool k2 = FMT == QW_FMT_2BIT_G32, kN = FMT == QW_FMT_NF4_B64;
+  constexpr bool k2 = FMT == QW_FMT_2BIT_G32, kN = FMT == QW_FMT_NF4_B64, k4 = FMT == QW_FMT_INT4_G32;
   constexpr int kRows = 16 * MR;
   constexpr int kPieces = kRows * 8 / kThreads;  // 16-byte pieces of X per thread and stage
   constexpr int kSpan = k2 ? 256 : 128;          // weights of a column in one set of code loads
@@ -48,7 +48,7 @@ __global__ __launch_bounds__(kThreads, 2) void wide_kernel(ExpertArgs a) {
   constexpr int kCodeDiv = k2 ? 4 : 2, kScaleDiv = k2 ? 8 : 16;
   static_assert(kPieces >= 1, "every thread copies a piece");
 
-  __shared__ __attribute__((aligned(16))) char tab[256 * kEntry];
+  __shared__ __attribute__((aligned(16))) char tab[k4 ? 16 : 256 * kEntry];
   // the X buffers; behind the loop the waves' slabs lie there
   constexpr int kBuf = kRows * kStage * 2, kSlabLd = kSub * 16 + 4;
   constexpr int kSlab = kWaves * 16 * kSlabLd * 4;
@@ -63,7 +63,7 @@ __global__ __launch_bounds__(kThreads, 2) void wide_kernel(ExpertArgs a) {
   if (at.rows.cnt == 0) return;
   const RowTile rt = at.rows;
   const int e = rt.g;
-  fill_table<FMT, DT, kThreads, true>(tab, a);
+  if (!k4) fill_table<FMT, DT, kThreads, true>(tab, a);
 
   // ---- X: this thread's pieces; rows past the tile repeat its first row ----
   const int pc = tid & 7, pr = tid >> 3;
@@ -99,6 +99,7 @@ __global__ __launch_bounds__(kThreads, 2) void wide_kernel(ExpertArgs a) {
         if (k2 && ANCH) keep &= ~(((drop >> (2 * q)) & 1 ? 0xFFFFu : 0u) | ((drop >> (2 * q + 1)) & 1 ? 0xFFFF0000u : 0u));
         v[q] &= keep;
       }
+      if (k4) v = Int4<DT>::order(v);
       *reinterpret_cast<u32x4 *>(xs + buf * kBuf + xat[i]) = v;
     }
   };
@@ -156,6 +157,8 @@ __global__ __launch_bounds__(kThreads, 2) void wide_kernel(ExpertArgs a) {
     }
   };
   const uint32_t rep = k2 ? (uint32_t)(lane & 15) * 8u : (uint32_t)(lane & 31) * 4u;
+  uint32_t sixteen = Int4<DT>::kSixteen;
+  if (k4) asm volatile("" : "+v"(sixteen));  // an and-or takes one scalar operand
   // operand of column block j for step h of stage s of the set
   auto make_b = [&](const Set &d, int j, int s, int h) {
     if (k2) {
@@ -165,6 +168,7 @@ __global__ __launch_bounds__(kThreads, 2) void wide_kernel(ExpertArgs a) {
       return u32x4{lo[0], lo[1], hi[0], hi[1]};
     }
     const uint32_t c = d.c[j][2 * (s & 1) + h];
+    if (k4) return Int4<DT>::operand(c, sixteen);
     u32x4 b;
 #pragma unroll
     for (int q = 0; q < 4; ++q) b[q] = *reinterpret_cast<const uint32_t *>(tab + ((((c >> (8 * q)) & 0xFFu) << 7) | rep));
@@ -219,10 +223,12 @@ __global__ __launch_bounds__(kThreads, 2) void wide_kernel(ExpertArgs a) {
           const u32x4 x = read_a(buf, i, h);
           u32x4 x1;
           if (kN) x1 = read_a(buf, i, 1);
+          constexpr uint32_t m24 = Int4<DT>::kMinus24;
+          const f32x4 start = k4 ? O::mma(x, u32x4{m24, m24, m24, m24}, zero) : zero;
 #pragma unroll
           for (int j = 0; j < kSub; ++j) {
             f32x4 &t = dd[i & 1][j];
-            t = O::mma(x, b[0][j], zero);
+            t = O::mma(x, b[0][j], start);
             if (kN) t = O::mma(x1, b[kN ? 1 : 0][j], t);
           }
         }

@@ -51,6 +51,20 @@ __device__ inline RowTile find_row_tile(const int32_t *offsets, int G, int n, in
   return RowTile{0, 0, 0};
 }
 
+// rows[] by position. Few rows are read at once, one a lane, before the
+// position is known: a short launch is a chain of dependent loads from cold
+// memory (a microsecond each), of which this takes one out. Made and asked
+// by whole waves; p must be in 0..n-1.
+struct RowLookup {
+  const int32_t *rows;
+  bool small;
+  int mine;
+  __device__ RowLookup(const int32_t *r, int n) : rows(r), small(n <= 64), mine(0) {
+    if (small) mine = r[min((int)(threadIdx.x & 63), n - 1)];
+  }
+  __device__ int operator()(int p) const { return small ? __shfl(mine, p, 64) : rows[p]; }
+};
+
 // Number of those tiles, wave-uniform.
 __device__ inline int count_row_tiles(const int32_t *offsets, int G, int n, int height) {
   int own = 0;
