@@ -2,7 +2,7 @@
 //
 // Top-k: a token's E logits lie in V registers of L lanes (element v L +
 // lane). Each of the k rounds takes the largest (logit, lowest index) by a
-// maximum over the lane's V keys and a butterfly of log2 L lane exchanges,
+// maximum over the lane's V keys and log2 L exchanges between lanes,
 // and clears the taken one. A key is the logit mapped to an integer of the
 // same order with the inverted index behind it, so one integer maximum
 // decides ties: 32 bits for the 16-bit types, 64 for fp32.
@@ -38,6 +38,54 @@ __device__ inline float from_ordered32(uint32_t k) {
   return __builtin_bit_cast(float, (k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
 }
 
+// The largest of v over the L lanes of a token, in every one of them. Row
+// operations and half swaps in place of lane permutes through LDS, whose
+// latency would be most of the time of a round.
+template <int CTRL, typename T>
+__device__ inline T row_max(T v) {
+  T o;
+  if constexpr (sizeof(T) == 8) {
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)v, CTRL, 0xF, 0xF, true);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(v >> 32), CTRL, 0xF, 0xF, true);
+    o = (T)hi << 32 | lo;
+  } else {
+    o = (T)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true);
+  }
+  return o > v ? o : v;
+}
+template <bool HALVES, typename T>
+__device__ inline T swap_max(T v) {
+  auto swap = [](uint32_t w, uint32_t &a, uint32_t &b) {
+    if constexpr (HALVES) {
+      const auto r = __builtin_amdgcn_permlane32_swap(w, w, false, false);
+      a = r[0], b = r[1];
+    } else {
+      const auto r = __builtin_amdgcn_permlane16_swap(w, w, false, false);
+      a = r[0], b = r[1];
+    }
+  };
+  uint32_t a, b;
+  swap((uint32_t)v, a, b);
+  if constexpr (sizeof(T) == 8) {
+    uint32_t c, d;
+    swap((uint32_t)(v >> 32), c, d);
+    const T x = (T)c << 32 | a, y = (T)d << 32 | b;
+    return x > y ? x : y;
+  } else {
+    return a > b ? a : b;
+  }
+}
+template <int L, typename T>
+__device__ inline T lanes_max(T v) {
+  v = row_max<0xB1>(v);              // quad permute 1 0 3 2
+  v = row_max<0x4E>(v);              // quad permute 2 3 0 1
+  v = row_max<0x141>(v);             // mirror in half rows
+  if constexpr (L >= 16) v = row_max<0x140>(v);  // mirror in rows
+  if constexpr (L >= 32) v = swap_max<false>(v);
+  if constexpr (L >= 64) v = swap_max<true>(v);
+  return v;
+}
+
 // 16-bit logits: the upper half of the fp32 pattern (bf16), or the fp16
 // pattern itself, above the inverted index.
 template <int DT>
@@ -56,7 +104,6 @@ struct Keys {
     const uint32_t h = o < 0x8000u ? (0x8000u - o) | 0x8000u : o - 0x8000u;
     return DT == QW_DT_BF16 ? __builtin_bit_cast(float, h << 16) : f16_bits_to_f32((uint16_t)h);
   }
-  static __device__ key_t exchange(key_t k, int d, int width) { return __shfl_xor(k, d, width); }
 };
 template <>
 struct Keys<QW_DT_F32> {
@@ -67,7 +114,6 @@ struct Keys<QW_DT_F32> {
   }
   static __device__ int index(key_t k) { return (int)(0xFFFFFFFFu - (uint32_t)k); }
   static __device__ float value(key_t k) { return from_ordered32((uint32_t)(k >> 32)); }
-  static __device__ key_t exchange(key_t k, int d, int width) { return __shfl_xor(k, d, width); }
 };
 
 struct RouteArgs {
@@ -99,11 +145,7 @@ __device__ inline void topk_tokens(const RouteArgs &a, int t0, int count, int32_
       typename KT::key_t best = key[0];
 #pragma unroll
       for (int v = 1; v < V; ++v) best = key[v] > best ? key[v] : best;
-#pragma unroll
-      for (int d = L / 2; d; d >>= 1) {
-        const typename KT::key_t o = KT::exchange(best, d, L);
-        best = o > best ? o : best;
-      }
+      best = lanes_max<L>(best);
       const float val = KT::value(best);
       if (j == 0) {
         top = val;
@@ -296,7 +338,7 @@ __global__ __launch_bounds__(kThreads) void place_kernel(GroupArgs g) {
   if (G <= kThreads ? part < parts : true) {
     for (int e = G <= kThreads ? threadIdx.x % G : threadIdx.x; e < G; e += kThreads) {
       int all = 0, before = 0;
-#pragma unroll 8
+#pragma unroll 16
       for (int q = G <= kThreads ? part : 0; q < g.blocks; q += parts) {
         const int c = g.counts[(size_t)q * G + e];
         all += c;

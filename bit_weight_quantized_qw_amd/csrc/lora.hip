@@ -54,6 +54,7 @@ __global__ __launch_bounds__(kThreads) void shrink_kernel(LoraArgs a) {
   const int split = b % a.splits;
   b /= a.splits;
   const int rt0 = b % a.rank_tiles * (RB * 16);
+  const RowLookup row_at(a.rows, a.n);
   const RowTile t = find_row_tile(a.offsets, a.G, a.n, MR * 16, b / a.rank_tiles);
   if (t.cnt == 0) return;
   const int K = a.K;
@@ -64,7 +65,7 @@ __global__ __launch_bounds__(kThreads) void shrink_kernel(LoraArgs a) {
 #pragma unroll
   for (int i = 0; i < MR; ++i) {
     const int q = i * 16 + ln;
-    int m = a.rows[t.p0 + (q < t.cnt ? q : 0)];
+    int m = row_at(t.p0 + (q < t.cnt ? q : 0));
     if ((uint32_t)m >= (uint32_t)a.n) m = 0;
     xp[i] = a.x + (size_t)m * K + lg * 16;
   }
@@ -135,28 +136,6 @@ __device__ inline void store_as(void *p, size_t i, int dt, float v) {
   else
     reinterpret_cast<uint16_t *>(p)[i] = (uint16_t)out_bits(v, dt);
 }
-// 16 consecutive elements (16-byte aligned rows)
-__device__ inline void load16(const void *p, size_t i, int dt, float (&v)[16]) {
-  if (dt == QW_DT_F32) {
-    const f32x4 *q = reinterpret_cast<const f32x4 *>(reinterpret_cast<const float *>(p) + i);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const f32x4 w = q[k];
-      v[4 * k] = w[0]; v[4 * k + 1] = w[1]; v[4 * k + 2] = w[2]; v[4 * k + 3] = w[3];
-    }
-  } else {
-    const u32x4 *q = reinterpret_cast<const u32x4 *>(reinterpret_cast<const uint16_t *>(p) + i);
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const u32x4 w = q[k];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        v[8 * k + 2 * e] = dt == QW_DT_F16 ? Op<QW_DT_F16>::value(w[e] & 0xFFFFu) : Op<QW_DT_BF16>::value(w[e] & 0xFFFFu);
-        v[8 * k + 2 * e + 1] = dt == QW_DT_F16 ? Op<QW_DT_F16>::value(w[e] >> 16) : Op<QW_DT_BF16>::value(w[e] >> 16);
-      }
-    }
-  }
-}
 __device__ inline void store16(void *p, size_t i, int dt, const float (&v)[16]) {
   if (dt == QW_DT_F32) {
     f32x4 *q = reinterpret_cast<f32x4 *>(reinterpret_cast<float *>(p) + i);
@@ -179,21 +158,67 @@ __device__ inline void store16(void *p, size_t i, int dt, const float (&v)[16]) 
 // of B_a as the first operand), and block j of a wave's four holds the
 // columns 16 g + 4 j .. + 3 of lane group g, so a lane ends with 16
 // consecutive columns of one row: 16-byte loads and stores straight from
-// the registers.
-template <int DT, int MR>
-__global__ __launch_bounds__(kThreads) void expand_kernel(LoraArgs a) {
+// the registers. B32: base is fp32.
+//
+// A decode step is a chain of dependent loads (offsets, rows, then base, B
+// and t), so the base and the first 64 inner elements of B are requested
+// before t is put together.
+template <int DT, int MR, bool B32>
+__global__ __launch_bounds__(kThreads, 2) void expand_kernel(LoraArgs a) {
   using O = Op<DT>;
   extern __shared__ __attribute__((aligned(16))) uint16_t smem[];  // [2][MR * 16][ld]
   __shared__ float unit[MR * 16];  // scale times the row's power of two
   const int tid = threadIdx.x, lane = tid & 63, ln = lane & 15, lg = lane >> 4;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int cg = blockIdx.x % a.col_groups;
+  const RowLookup row_at(a.rows, a.n);
   const RowTile t = find_row_tile(a.offsets, a.G, a.n, MR * 16, blockIdx.x / a.col_groups, true);
   if (t.cnt == 0) return;
   const bool rest = t.g == a.G;  // rows without an adapter: base alone
   if (rest && a.in_place) return;
   const int r = a.r, rp = (r + 31) & ~31, ld = rp + 8;
   uint16_t *const hi = smem, *const lo = smem + MR * 16 * ld;
+
+  int m[MR];
+#pragma unroll
+  for (int i = 0; i < MR; ++i) {
+    const int q = i * 16 + ln;
+    m[i] = row_at(t.p0 + min(q, t.cnt - 1));
+    if (q >= t.cnt || (uint32_t)m[i] >= (uint32_t)a.n) m[i] = -1;
+  }
+  const bool vec = a.N % 8 == 0;  // every row starts on 16 bytes in both types
+
+  // the loads of one column run: base, and B's first two steps of 32
+  u32x4 raw[MR][B32 ? 4 : 2], w[2][4];
+  const uint16_t *bp[4];
+  bool in[4];
+  auto request = [&](int ct) {
+    const int c0 = (cg * a.cols_per_group + ct) * kColTile + wv * 64;
+    const int c = c0 + lg * 16;
+    if (vec && c + 16 <= a.N) {
+#pragma unroll
+      for (int i = 0; i < MR; ++i) {
+        const size_t o = (size_t)max(m[i], 0) * a.N + c;
+        const u32x4 *p = reinterpret_cast<const u32x4 *>(
+            B32 ? reinterpret_cast<const char *>(reinterpret_cast<const float *>(a.base) + o)
+                : reinterpret_cast<const char *>(reinterpret_cast<const uint16_t *>(a.base) + o));
+#pragma unroll
+        for (int k = 0; k < (B32 ? 4 : 2); ++k) raw[i][k] = p[k];
+      }
+    }
+    if (rest) return;
+    // row q of block j is column 16 (q / 4) + 4 j + q % 4
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int cb = c0 + 16 * (ln >> 2) + 4 * j + (ln & 3);
+      in[j] = cb < a.N;
+      bp[j] = a.B + ((size_t)t.g * a.N + (in[j] ? cb : 0)) * r + lg * 8;
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+        w[s][j] = s * 32 + lg * 8 < r && in[j] ? *reinterpret_cast<const u32x4 *>(bp[j] + s * 32) : u32x4{0, 0, 0, 0};
+    }
+  };
+  request(0);
 
   // t of the tile: 16 lanes a row, each 8 of every 128 inner values
   if (!rest) {
@@ -247,15 +272,6 @@ __global__ __launch_bounds__(kThreads) void expand_kernel(LoraArgs a) {
     __syncthreads();
   }
 
-  int m[MR];
-#pragma unroll
-  for (int i = 0; i < MR; ++i) {
-    const int q = i * 16 + ln;
-    m[i] = q < t.cnt ? a.rows[t.p0 + q] : -1;
-    if ((uint32_t)m[i] >= (uint32_t)a.n) m[i] = -1;
-  }
-  const bool vec = a.N % 8 == 0;  // every row starts on 16 bytes in both types
-
   for (int ct = 0; ct < a.cols_per_group; ++ct) {
     const int c0 = (cg * a.cols_per_group + ct) * kColTile + wv * 64;
     if (c0 >= a.N) return;
@@ -264,31 +280,26 @@ __global__ __launch_bounds__(kThreads) void expand_kernel(LoraArgs a) {
     for (int i = 0; i < MR; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
-    if (!rest) {
-      // row q of block j is column 16 (q / 4) + 4 j + q % 4
-      const uint16_t *bp[4];
-      bool in[4];
+    auto product = [&](int k, const u32x4 (&b)[4]) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int c = c0 + 16 * (ln >> 2) + 4 * j + (ln & 3);
-        in[j] = c < a.N;
-        bp[j] = a.B + ((size_t)t.g * a.N + (in[j] ? c : 0)) * r + lg * 8;
+      for (int i = 0; i < MR; ++i) {
+        const u32x4 h = *reinterpret_cast<const u32x4 *>(hi + (i * 16 + ln) * ld + k + lg * 8);
+        const u32x4 l = *reinterpret_cast<const u32x4 *>(lo + (i * 16 + ln) * ld + k + lg * 8);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = O::mma(b[j], l, acc[i][j]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = O::mma(b[j], h, acc[i][j]);
       }
-#pragma unroll 2
-      for (int k = 0; k < rp; k += 32) {
-        u32x4 w[4];
+    };
+    if (!rest) {
+      product(0, w[0]);
+      if (rp > 32) product(32, w[1]);
+      for (int k = 64; k < rp; k += 32) {
+        u32x4 b[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          w[j] = k + lg * 8 < r && in[j] ? *reinterpret_cast<const u32x4 *>(bp[j] + k) : u32x4{0, 0, 0, 0};
-#pragma unroll
-        for (int i = 0; i < MR; ++i) {
-          const u32x4 h = *reinterpret_cast<const u32x4 *>(hi + (i * 16 + ln) * ld + k + lg * 8);
-          const u32x4 l = *reinterpret_cast<const u32x4 *>(lo + (i * 16 + ln) * ld + k + lg * 8);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) acc[i][j] = O::mma(w[j], l, acc[i][j]);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) acc[i][j] = O::mma(w[j], h, acc[i][j]);
-        }
+          b[j] = k + lg * 8 < r && in[j] ? *reinterpret_cast<const u32x4 *>(bp[j] + k) : u32x4{0, 0, 0, 0};
+        product(k, b);
       }
     }
     const int c = c0 + lg * 16;
@@ -300,10 +311,16 @@ __global__ __launch_bounds__(kThreads) void expand_kernel(LoraArgs a) {
         const float u = rest ? 0.0f : unit[i * 16 + ln];
         if (vec && c + 16 <= a.N) {
           float v[16];
-          load16(a.base, o, a.base_dtype, v);
-          if (!rest) {
 #pragma unroll
-            for (int q = 0; q < 16; ++q) v[q] = __builtin_fmaf(u, acc[i][q >> 2][q & 3], v[q]);
+          for (int q = 0; q < 16; ++q) {
+            if (B32) {
+              const uint32_t b32 = raw[i][q >> 2][q & 3];
+              v[q] = __builtin_bit_cast(float, b32);
+            } else {
+              const uint32_t b16 = (raw[i][(q >> 3) & 1][(q >> 1) & 3] >> (16 * (q & 1))) & 0xFFFFu;
+              v[q] = a.base_dtype == QW_DT_F16 ? Op<QW_DT_F16>::value(b16) : Op<QW_DT_BF16>::value(b16);
+            }
+            if (!rest) v[q] = __builtin_fmaf(u, acc[i][q >> 2][q & 3], v[q]);
           }
           store16(a.out, o, a.out_dtype, v);
         } else {
@@ -318,11 +335,13 @@ __global__ __launch_bounds__(kThreads) void expand_kernel(LoraArgs a) {
         }
       }
     }
+    if (ct + 1 < a.cols_per_group) request(ct + 1);
   }
 }
 
 // Row tiles of 64 once the adapters have some 24 rows each, so that the
-// adapters are read by fewer workgroups; else 16.
+// adapters are read by fewer workgroups (A x of 4001 rows, K = 4096, rank
+// 64: 16 us, 20 with tiles of 32); else 16.
 int row_blocks(int n, int G) { return n >= 24 * G ? 4 : 1; }
 
 // Splits of K: enough workgroups to fill the card, of at least four steps
@@ -331,7 +350,7 @@ int k_splits(const qw_adapters *ad, int n, int *per) {
   const int steps = (ad->K + kStep - 1) / kStep;
   const int rank_tiles = (ad->r + 63) / 64;
   const long long tiles = most_row_tiles(n, ad->count, 16 * row_blocks(n, ad->count)) * rank_tiles;
-  long long splits = (512 + tiles - 1) / tiles;
+  long long splits = (384 + tiles - 1) / tiles;
   if (splits > steps / 4) splits = steps / 4;
   if (splits > 16) splits = 16;
   if (splits < 1) splits = 1;
@@ -349,10 +368,15 @@ qw_status launch_lora(LoraArgs a, hipStream_t s) {
   const long long tiles = most_row_tiles(a.n, a.G, MR * 16);
   const long long g1 = tiles * a.rank_tiles * a.splits;
   const int col_tiles = (a.N + kColTile - 1) / kColTile;
-  const long long tiles2 = most_row_tiles(a.n, a.G + 1, MR * 16);
-  // several column runs per workgroup once there are workgroups enough, so
-  // that t is read and split fewer times
-  long long per = tiles2 * col_tiles / 1024;
+  // the second launch takes half as many rows a workgroup: its registers
+  // hold base, B and the sums, and three waves a SIMD keep more in flight
+  // than two (4001 rows x 11008, rank 64: 62 us against 70)
+  constexpr int ME = MR > 1 ? MR / 2 : 1;
+  const long long tiles2 = most_row_tiles(a.n, a.G + 1, ME * 16);
+  // several column runs per workgroup once there are three workgroups a CU,
+  // so that t is read and split fewer times (64 rows x 13824 by 32 adapters:
+  // 10 us; 14 both with a run per workgroup and with half as many workgroups)
+  long long per = tiles2 * col_tiles / 768;
   a.cols_per_group = (int)(per < 1 ? 1 : per > 8 ? 8 : per);
   a.col_groups = (col_tiles + a.cols_per_group - 1) / a.cols_per_group;
   const long long g2 = tiles2 * a.col_groups;
@@ -363,10 +387,10 @@ qw_status launch_lora(LoraArgs a, hipStream_t s) {
     QW_HIP_TRY(launch(shrink_kernel<DT, MR, 2>, (unsigned)g1, kThreads, 0, s, a));
   else
     QW_HIP_TRY(launch(shrink_kernel<DT, MR, 4>, (unsigned)g1, kThreads, 0, s, a));
-  const size_t lds = (size_t)2 * MR * 16 * (((a.r + 31) & ~31) + 8) * 2;
-  QW_HIP_TRY(hipFuncSetAttribute(reinterpret_cast<const void *>(&expand_kernel<DT, MR>),
-                                 hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds));
-  QW_HIP_TRY(launch(expand_kernel<DT, MR>, (unsigned)g2, kThreads, lds, s, a));
+  const size_t lds = (size_t)2 * ME * 16 * (((a.r + 31) & ~31) + 8) * 2;
+  const auto expand = a.base_dtype == QW_DT_F32 ? expand_kernel<DT, ME, true> : expand_kernel<DT, ME, false>;
+  QW_HIP_TRY(hipFuncSetAttribute(reinterpret_cast<const void *>(expand), hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds));
+  QW_HIP_TRY(launch(expand, (unsigned)g2, kThreads, lds, s, a));
   return QW_OK;
 }
 

@@ -692,18 +692,23 @@ class Stack:
 
 # ------------------------------------------- rows that take different matrices
 
-def _same_device(*tensors):
-    """All tensors contiguous on the current device: the library launches
-    there, on the current stream."""
+_raw_stream = None
+
+
+def _here(*tensors):
+    """The current stream of the current device, on which all tensors have to
+    lie, contiguous: the library launches there."""
+    global _raw_stream
     import torch
     here = torch.cuda.current_device()
     for t in tensors:
-        if t is None:
-            continue
-        if not t.is_cuda or not t.is_contiguous():
-            raise ValueError("tensors must be contiguous CUDA tensors")
-        if t.device.index != here:
-            raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{here}")
+        if t.get_device() != here or not t.is_contiguous():
+            raise ValueError(f"tensors must be contiguous on the current device cuda:{here} (one is on {t.device}, "
+                             f"contiguous: {t.is_contiguous()})")
+    if _raw_stream is None:  # the stream's handle without a Stream object around it, where torch gives it
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda d: torch.cuda.current_stream(d).cuda_stream)
+    return _raw_stream(here)
 
 
 def _bytes_of(t):
@@ -739,6 +744,8 @@ class RowGroups:
         _need(rows, torch.int32, "rows", 1)
         if offsets.numel() < 2 or rows.numel() < 1:
             raise ValueError("offsets has G + 1 >= 2 entries, rows n >= 1")
+        if offsets.device != rows.device:
+            raise ValueError("offsets and rows are on different devices")
         self.offsets, self.rows = offsets, rows
         self.G, self.n = offsets.numel() - 1, rows.numel()
         self._c = qw_groups(self.G, self.n, offsets.data_ptr(), rows.data_ptr())
@@ -763,11 +770,11 @@ def qw_group_rows(ids, G, workspace=None):
     _need(ids, torch.int32, "ids", 1)
     n = ids.numel()
     ws = _workspace(workspace, qw_group_rows_workspace_bytes(n, G), ids.device)
-    _same_device(ids, ws)
+    stream = _here(ids, ws)
     offsets = torch.empty(G + 1, dtype=torch.int32, device=ids.device)
     rows = torch.empty(n, dtype=torch.int32, device=ids.device)
-    _check(lib().qw_group_rows(_ptr(ids), n, int(G), _ptr(offsets), _ptr(rows), _ptr(ws), ws.numel(), _stream()),
-           "qw_group_rows")
+    _check(lib().qw_group_rows(ids.data_ptr(), n, int(G), offsets.data_ptr(), rows.data_ptr(), ws.data_ptr(),
+                               ws.numel(), stream), "qw_group_rows")
     return RowGroups(offsets, rows)
 
 
@@ -782,17 +789,18 @@ def qw_route_topk(logits, top_k, normalize=True, workspace=None):
     dt = _need_any(logits, "logits", 2)
     T, E = logits.shape
     top_k = int(top_k)
-    ws = _workspace(workspace, qw_route_workspace_bytes(T, E, top_k), logits.device)
-    _same_device(logits, ws)
     if not 1 <= top_k <= E:
         raise ValueError("top_k must be in 1..E")
     dev = logits.device
+    ws = _workspace(workspace, qw_route_workspace_bytes(T, E, top_k), dev)
+    stream = _here(logits, ws)
     ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
     weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
     offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
     rows = torch.empty(T * top_k, dtype=torch.int32, device=dev)
-    _check(lib().qw_route_topk(_ptr(logits), dt, T, E, top_k, 1 if normalize else 0, _ptr(ids), _ptr(weights),
-                               _ptr(offsets), _ptr(rows), _ptr(ws), ws.numel(), _stream()), "qw_route_topk")
+    _check(lib().qw_route_topk(logits.data_ptr(), dt, T, E, top_k, 1 if normalize else 0, ids.data_ptr(),
+                               weights.data_ptr(), offsets.data_ptr(), rows.data_ptr(), ws.data_ptr(), ws.numel(),
+                               stream), "qw_route_topk")
     return Routing(ids, weights, RowGroups(offsets, rows))
 
 
@@ -822,6 +830,8 @@ class ExpertWeights:
                 t = torch.empty(nb, dtype=torch.uint8, device=device)
                 t = t.view(torch.int16) if name == "out_w" else t.view(torch.int32) if name.startswith("out_") else t
             setattr(self, name, t)
+        if len({t.device for t in (self.codes, self.scales, self.out_idx, self.out_w, self.out_mask) if t is not None}) > 1:
+            raise ValueError("the experts' buffers are on different devices")
         p = lambda t: t.data_ptr() if t is not None else None
         self._c = qw_experts(E, qw_weight(fmt, N, K, n_out, self.n_out_pad, p(self.codes), p(self.scales),
                                           p(self.out_idx), p(self.out_w), p(self.out_mask)))
@@ -871,9 +881,10 @@ def qgemm_experts(ew, X, groups, top_k=1, swiglu=False, out_dtype=None, out=None
     Y = out if out is not None else torch.empty((groups.n, N), dtype=out_dtype or X.dtype, device=X.device)
     if tuple(Y.shape) != (groups.n, N):
         raise ValueError(f"output shape {tuple(Y.shape)}, expected {(groups.n, N)}")
-    _same_device(X, Y, groups.offsets, groups.rows, ew.codes)
-    _check(lib().qgemm_experts(ctypes.byref(ew._c), _ptr(X), _dt(X.dtype), X.shape[0], div, ctypes.byref(groups._c),
-                               1 if swiglu else 0, _ptr(Y), _dt(Y.dtype), _stream()), "qgemm_experts")
+    stream = _here(X, Y, groups.offsets, ew.codes)
+    _check(lib().qgemm_experts(ctypes.byref(ew._c), X.data_ptr(), _dt(X.dtype), X.shape[0], div,
+                               ctypes.byref(groups._c), 1 if swiglu else 0, Y.data_ptr(), _w_dtype(Y), stream),
+           "qgemm_experts")
     return Y
 
 
@@ -896,10 +907,10 @@ def qgemm_experts_combine(ew, H, groups, ids, weights, out_dtype=None, out=None,
     if tuple(Y.shape) != (T, ew.N):
         raise ValueError(f"output shape {tuple(Y.shape)}, expected {(T, ew.N)}")
     ws = _workspace(workspace, qw_experts_combine_workspace_bytes(ew.N, T, k), H.device)
-    _same_device(H, Y, ids, weights, ws, groups.offsets, groups.rows, ew.codes)
-    _check(lib().qgemm_experts_combine(ctypes.byref(ew._c), _ptr(H), _dt(H.dtype), ctypes.byref(groups._c), _ptr(ids),
-                                       _ptr(weights), T, k, _ptr(Y), _dt(Y.dtype), _ptr(ws), ws.numel(), _stream()),
-           "qgemm_experts_combine")
+    stream = _here(H, Y, ids, weights, ws, groups.offsets, ew.codes)
+    _check(lib().qgemm_experts_combine(ctypes.byref(ew._c), H.data_ptr(), _dt(H.dtype), ctypes.byref(groups._c),
+                                       ids.data_ptr(), weights.data_ptr(), T, k, Y.data_ptr(), _w_dtype(Y),
+                                       ws.data_ptr(), ws.numel(), stream), "qgemm_experts_combine")
     return Y
 
 
@@ -919,6 +930,8 @@ class Adapters:
         self.N = B.shape[1]
         if B.shape[0] != self.count or B.shape[2] != self.r or scale.numel() != self.count:
             raise ValueError("A (count, r, K), B (count, N, r) and scale (count,) do not fit together")
+        if B.device != A.device or scale.device != A.device:
+            raise ValueError("A, B and scale are on different devices")
         self.A, self.B, self.scale, self.dtype = A, B, scale, A.dtype
         self._c = qw_adapters(self.count, self.N, self.K, self.r, _dt(A.dtype), A.data_ptr(), B.data_ptr(),
                               scale.data_ptr())
@@ -944,7 +957,8 @@ def qw_lora_add(adapters, x, groups, base, out_dtype=None, out=None, workspace=N
     if tuple(Y.shape) != (n, adapters.N):
         raise ValueError(f"output shape {tuple(Y.shape)}, expected {(n, adapters.N)}")
     ws = _workspace(workspace, qw_lora_workspace_bytes(adapters, n), x.device)
-    _same_device(x, base, Y, ws, groups.offsets, groups.rows, adapters.A, adapters.B, adapters.scale)
-    _check(lib().qw_lora_add(ctypes.byref(adapters._c), _ptr(x), ctypes.byref(groups._c), _ptr(base), _dt(base.dtype),
-                             _ptr(Y), _dt(Y.dtype), _ptr(ws), ws.numel(), _stream()), "qw_lora_add")
+    stream = _here(x, base, Y, ws, groups.offsets, adapters.A)
+    _check(lib().qw_lora_add(ctypes.byref(adapters._c), x.data_ptr(), ctypes.byref(groups._c), base.data_ptr(),
+                             _w_dtype(base), Y.data_ptr(), _w_dtype(Y), ws.data_ptr(), ws.numel(), stream),
+           "qw_lora_add")
     return Y
