@@ -43,7 +43,7 @@ _MC = [_C + "gemv2_mfma.hip", _C + "gemv2.hip", _C + "qw_internal.h"]
 _VALU = [_C + "gemv2_kernel.h", _C + "gemv2_b1.hip", _C + "gemv2.hip", _C + "qw_internal.h"]
 _NF4 = [_C + "gemv_nf4.hip", _C + "qw_internal.h"]
 _INT4 = [_C + "gemv2_mfma.hip", _C + "gemv_int4.hip", _C + "qw_internal.h"]
-_PF = [_C + "prefill.hip", _C + "qw_internal.h"]
+_PF = [_C + "prefill.hip", _C + "prefill_w.h", _C + "op16.h", _C + "row_groups.h", _C + "qw_internal.h"]
 
 # workload -> bench kernel -> (dispatches of one call: [(name substring, grid
 # in threads or None)], dispatches per call, sources hashed). The grids tell
