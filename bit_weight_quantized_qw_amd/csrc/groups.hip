@@ -367,21 +367,39 @@ __global__ __launch_bounds__(kThreads) void place_kernel(GroupArgs g) {
   place_slots(l, slots, s0, G, g.rows);
 }
 
-// Slots of a block: all of them up to kSlots, else 512 a block (two passes
-// of the top-k at 16 lanes a token) until the counts that every block adds
-// up would be the larger cost, at most kSlots.
-int block_slots(long long n, int unit) {
+// Rows of a block of qw_group_rows: all of them up to kSlots, else 512 until
+// the counts that every block adds up would be the larger cost, at most
+// kSlots.
+int block_rows(long long n) {
   long long per = n <= kSlots ? n : 512;
   while (per < kSlots && n > per * 256) per *= 2;
-  per = per / unit * unit;
-  if (per < unit) per = unit;
   return (int)per;
 }
 
-size_t counts_bytes(long long n, int G, int unit) {
-  if (n <= kSlots / unit * unit) return 0;
-  const long long per = block_slots(n, unit);
-  return (size_t)((n + per - 1) / per) * (size_t)G * sizeof(int32_t);
+// Lanes a token takes in the top-k: enough that a lane holds at most 8
+// logits (16 beyond 512 experts) and that every choice has a lane to keep
+// it; fewer lanes mean more tokens side by side and fewer exchanges.
+int topk_lanes(int E, int k) {
+  if (E <= 32 && k <= 8) return 8;
+  if (E <= 128 && k <= 16) return 16;
+  return E <= 256 ? 32 : 64;
+}
+
+// Slots of a block of the router: all of them where they are at most kSlots
+// and the top-k takes few passes; else two passes of the top-k a block (16384
+// tokens of 8 in 128: 10 us, 17 with twice as many), more where there would
+// be over 256 blocks, at most kSlots. A multiple of k.
+int block_slots(int T, int E, int k) {
+  const int pass = kThreads / topk_lanes(E, k);
+  if (T <= 4 * pass && (long long)T * k <= kSlots) return T * k;
+  long long tokens = 2 * pass;
+  while (2 * tokens * k <= kSlots && T > tokens * 256) tokens *= 2;
+  while (tokens > 1 && tokens * k > kSlots) tokens /= 2;
+  return (int)(tokens * k);
+}
+
+size_t counts_bytes(long long n, int per, int G) {
+  return n <= per ? 0 : (size_t)((n + per - 1) / per) * (size_t)G * sizeof(int32_t);
 }
 
 qw_status launch_place(const GroupArgs &g, hipStream_t s) {
@@ -393,11 +411,9 @@ qw_status launch_place(const GroupArgs &g, hipStream_t s) {
 template <int DT>
 qw_status launch_route(const RouteArgs &a, const GroupArgs &g, hipStream_t s) {
   const size_t lds = group_lds_bytes(g.G);
-  // lanes per token: enough that a lane holds at most 8 logits (16 beyond
-  // 512 experts) and that every choice has a lane to keep it; fewer lanes
-  // mean more tokens side by side and fewer exchanges
+  const int lanes = topk_lanes(a.E, a.k);
 #define QW_ROUTE(L, V)                                                                \
-  if (a.E <= (L) * (V) && a.k <= (L)) {                                               \
+  if (lanes == (L) && a.E <= (L) * (V)) {                                             \
     QW_HIP_TRY(launch(route_kernel<DT, L, V>, g.blocks, kThreads, lds, s, a, g));     \
     return launch_place(g, s);                                                        \
   }
@@ -418,13 +434,13 @@ extern "C" {
 
 size_t qw_group_rows_workspace_bytes(int n, int G) {
   if (n < 1 || n > QW_MAX_ROWS || G < 1 || G > QW_MAX_GROUPS) return 0;
-  return qw::counts_bytes(n, G, 1);
+  return qw::counts_bytes(n, qw::block_rows(n), G);
 }
 
 size_t qw_route_workspace_bytes(int T, int E, int top_k) {
   if (T < 1 || E < 1 || E > QW_MAX_GROUPS || top_k < 1 || top_k > E || top_k > QW_MAX_TOPK) return 0;
   const long long n = (long long)T * top_k;
-  return n <= QW_MAX_ROWS ? qw::counts_bytes(n, E, top_k) : 0;
+  return n <= QW_MAX_ROWS ? qw::counts_bytes(n, qw::block_slots(T, E, top_k), E) : 0;
 }
 
 qw_status qw_group_rows(const int32_t *ids, int n, int G, int32_t *offsets, int32_t *rows,
@@ -433,7 +449,8 @@ qw_status qw_group_rows(const int32_t *ids, int n, int G, int32_t *offsets, int3
   CallScope scope;
   if (!ids || !offsets || !rows || n < 1 || G < 1) return QW_ERR_INVALID_ARG;
   if (G > QW_MAX_GROUPS || n > QW_MAX_ROWS) return QW_ERR_UNSUPPORTED;
-  const size_t need = counts_bytes(n, G, 1);
+  const int per = block_rows(n);
+  const size_t need = counts_bytes(n, per, G);
   if (need && (!workspace || workspace_bytes < need)) return QW_ERR_INVALID_ARG;
   if (!aligned16(ids) || !aligned16(offsets) || !aligned16(rows) || (need && !aligned16(workspace)))
     return QW_ERR_ALIGNMENT;
@@ -445,8 +462,8 @@ qw_status qw_group_rows(const int32_t *ids, int n, int G, int32_t *offsets, int3
   g.counts = reinterpret_cast<int32_t *>(workspace);
   g.n = n;
   g.G = G;
-  g.per = block_slots(n, 1);
-  g.blocks = (int)(((long long)n + g.per - 1) / g.per);
+  g.per = per;
+  g.blocks = (int)(((long long)n + per - 1) / per);
   QW_HIP_TRY(launch(group_kernel, g.blocks, kThreads, group_lds_bytes(G), as_stream(stream), g));
   return launch_place(g, as_stream(stream));
 }
@@ -461,7 +478,8 @@ qw_status qw_route_topk(const void *logits, qw_dtype dtype, int T, int E, int to
   if (dtype != QW_DT_F16 && dtype != QW_DT_BF16 && dtype != QW_DT_F32) return QW_ERR_INVALID_ARG;
   const long long n = (long long)T * top_k;
   if (E > QW_MAX_GROUPS || n > QW_MAX_ROWS) return QW_ERR_UNSUPPORTED;
-  const size_t need = counts_bytes(n, E, top_k);
+  const int per = block_slots(T, E, top_k);
+  const size_t need = counts_bytes(n, per, E);
   if (need && (!workspace || workspace_bytes < need)) return QW_ERR_INVALID_ARG;
   if (!aligned16(logits) || !aligned16(ids) || !aligned16(weights) || !aligned16(offsets) ||
       !aligned16(rows) || (need && !aligned16(workspace)))
@@ -475,8 +493,8 @@ qw_status qw_route_topk(const void *logits, qw_dtype dtype, int T, int E, int to
   g.counts = reinterpret_cast<int32_t *>(workspace);
   g.n = (int)n;
   g.G = E;
-  g.per = block_slots(n, top_k);
-  g.blocks = (int)((n + g.per - 1) / g.per);
+  g.per = per;
+  g.blocks = (int)((n + per - 1) / per);
   if (dtype == QW_DT_F32) return launch_route<QW_DT_F32>(a, g, as_stream(stream));
   if (dtype == QW_DT_BF16) return launch_route<QW_DT_BF16>(a, g, as_stream(stream));
   return launch_route<QW_DT_F16>(a, g, as_stream(stream));
