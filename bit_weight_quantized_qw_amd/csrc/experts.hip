@@ -18,10 +18,18 @@
 //   2-bit: the levels +-1.52, +-0.45 enter as +-152, +-45 (exact in fp16
 //     and bf16), the sum is divided by 100 at the end; Z times the row sums
 //     of x, which come from the same A operand against a constant 100.
-//   INT4: u - 8 is exact. NF4: a level is two 16-bit numbers, the nearest
-//     and the rest, two products.
-// A code byte becomes 16-bit levels by one LDS table read. Lane l reads
-// replica l % 16 of the table, so no two of 16 lanes meet in a bank.
+//   INT4: 16 + u, made from the nibbles without a table, the products
+//     starting from -24 times the row sums of x. NF4: a level is two 16-bit
+//     numbers, the nearest and the rest, two products.
+// A code byte of the other formats becomes 16-bit levels by one LDS table
+// read. Lane l reads replica l % 16 of the table, so no two of 16 lanes meet
+// in a bank. Up to four rows, four scale groups share one result (below).
+//
+// Measured (kernel alone): 40 rows over 16 experts of 8192 x 4096 in NF4 80
+// us, 3.8 TB/s; 136 slots over 64 experts of 2048 x 1408 in 2-bit with
+// anchors 29 us, 2.8 TB/s; one token's 8 of 64 experts of 2816 x 2048 12 us,
+// of which 9 are one workgroup: 1 until its tile is known, 4 until its first
+// codes are there, 1.3 a chunk of 256 weights, 0.5 for the sums.
 //
 // A lane loads 64 consecutive codes of one column (16 bytes of 2-bit, 32 of
 // 4-bit codes); the matrix instruction wants eight per lane of 32

@@ -65,7 +65,8 @@ struct RowLookup {
   __device__ int operator()(int p) const { return small ? __shfl(mine, p, 64) : rows[p]; }
 };
 
-// Number of those tiles, wave-uniform.
+// Number of those tiles, wave-uniform; no more than ascending offsets can
+// make (what the grid was sized for), whatever the offsets are.
 __device__ inline int count_row_tiles(const int32_t *offsets, int G, int n, int height) {
   int own = 0;
   for (int g = threadIdx.x & 63; g < G; g += 64) {
@@ -74,7 +75,7 @@ __device__ inline int count_row_tiles(const int32_t *offsets, int G, int n, int 
   }
 #pragma unroll
   for (int d = 32; d; d >>= 1) own += __shfl_xor(own, d, 64);
-  return __builtin_amdgcn_readfirstlane(own);
+  return min(__builtin_amdgcn_readfirstlane(own), n / height + G);
 }
 
 // Most tiles that n rows in G groups can make: every group ends in at most

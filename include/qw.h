@@ -600,8 +600,10 @@ typedef struct {
  * qgemv_2bit_swiglu, Y being [n][I].
  *   X  device [x_rows][K] of x_dtype F16 or BF16 (x_rows >= g->n when x_div
  *      is 0); g->G == ew->E
- *   Y  device [g->n][N or I] of y_dtype F16, BF16 or F32, rounded once;
- *      rows of positions in no group are left as they were.
+ *   Y  device [g->n][N or I] of y_dtype F16, BF16 or F32, rounded once, not
+ *      overlapping X; rows of positions in no group are left as they were.
+ * Activations are finite: a row with an infinity or NaN gives values that
+ * are not, in that row alone.
  * fp32 accumulation. Gated products, experts with anchors, and any with
  * few rows per expert scale fp32 sums of exact code levels, so no weight is
  * rounded (NF4 levels are, to two numbers of x_dtype, or with more rows to
@@ -660,7 +662,8 @@ size_t qw_lora_workspace_bytes(const qw_adapters *ad, int n);
  *   out[m] = base[m] + scale[a] * B_a (A_a x[m]),   a the group of row m,
  * for every row of a group, rounded once to out's type; rows of no group
  * get base[m]. base may be a projection's fp32 output, so that the sum is
- * rounded once, and base == out (equal types) adds in place.
+ * rounded once, and base == out (equal types) adds in place (they are the
+ * same buffer or do not overlap).
  *   x    device [n][K] of ad->dtype, n = g->n; g->G == ad->count
  *   base device [n][N] of base_dtype, out device [n][N] of out_dtype (F16,
  *        BF16 or F32 each)

@@ -173,7 +173,7 @@ def test_offsets_that_do_not_fit_stay_in_bounds(blocks, tune):
     ex = Experts("nf4", 3, 40, 128, 0, seed=8)
     n = 20
     x = acts(np.random.default_rng(0), n, 128, torch.bfloat16)
-    for off in ([0, 5, 400, 500], [-7, 3, 2, 20], [0, 0, 0, 0], [20, 20, 20, 20]):
+    for off in ([0, 5, 400, 500], [-7, 3, 2, 20], [0, 0, 0, 0], [20, 20, 20, 20], [0, 20, 0, 20], [9, 0, 20, 1]):
         rows = np.arange(n, dtype=np.int32)
         rows[4] = 10**6
         rows[5] = -3
