@@ -520,29 +520,30 @@ qw_status launch_fmt(int fmt, const ExpertArgs &a, hipStream_t s) {
 //
 // A kernel's time is a start plus a share per 256 workgroups (one a CU),
 // the share (the narrow kernel's start too) growing with K; the tall tiles
-// go by whole rounds, each with its start. The rows per
+// go by rounds, whole ones where they are few, each with its start. The rows per
 // expert are on the device, so the number of row tiles is estimated: the
 // rows by the tile's height and 0.6 of a short tile per expert, at least one
 // for every expert that can have a row. The constants are fits, in us at K =
 // 2048, to 16 experts of 4096 columns with 16 to 512 rows each, 64 of 2816
 // and 8 of 1024 to 14336; measured / estimated for 2-bit, us:
 //     rows an expert        narrow     32 rows     64 rows    128 rows
-//     16 x 4096:  16        35 / 37    36 / 47     46 / 59    38 / 33
-//                 64        98 / 93    77 / 78     68 / 75    62 / 66
-//                128       173 / 166  117 / 119   101 / 103   65 / 66
-//                512                  365 / 368   268 / 270  165 / 165
-//      8 x 1024:  32        22 / 24    60 / 65     80 / 87    56 / 56
-//    (K = 4096)  128        56 / 52    65 / 65     84 / 87    61 / 56
-//     8 x 14336 (K = 4096) 1024 rows: 64 rows 1615, 128 rows 965, 256 rows 933
+//     16 x 4096:  16        35 / 37    36 / 47     46 / 59    38 / 34
+//                 64        98 / 93    77 / 78     68 / 75    62 / 68
+//                128       173 / 166  117 / 119   101 / 103   65 / 68
+//                512                  365 / 368   268 / 270  165 / 174
+//      8 x 1024:  32        22 / 24    60 / 65     80 / 87    56 / 64
+//    (K = 4096)  128        56 / 52    65 / 65     84 / 87    61 / 64
+//     8 x 14336 (K = 4096) 1024 rows: 64 rows 1615, 128 rows 965 to 1013 / 995,
+//     256 rows 933 / 992
 struct Cost {
   float start, share;
 };
 int pick_row_blocks(int fmt, const ExpertArgs &a, bool tall) {
   constexpr int kHeights[5] = {1, 2, 4, 8, 16};
   constexpr Cost kCost[3][5] = {
-      {{4, 4.6f}, {24, 20.7f}, {31, 27.8f}, {10, 23}, {8, 50}},  // 2-bit
-      {{4, 5.0f}, {23, 17.6f}, {28, 25.2f}, {12, 31}, {8, 64}},  // NF4
-      {{6, 5.2f}, {21, 17.8f}, {27, 25.7f}, {12, 26}, {8, 56}},  // INT4
+      {{4, 4.6f}, {24, 20.7f}, {31, 27.8f}, {4, 30}, {4, 56}},  // 2-bit
+      {{4, 5.0f}, {23, 17.6f}, {28, 25.2f}, {4, 39}, {4, 69}},  // NF4
+      {{6, 5.2f}, {21, 17.8f}, {27, 25.7f}, {4, 36}, {4, 62}},  // INT4
   };
   const Cost *cost = kCost[fmt == QW_FMT_2BIT_G32 ? 0 : fmt == QW_FMT_NF4_B64 ? 1 : 2];
   double least = 1e30;
@@ -552,7 +553,7 @@ int pick_row_blocks(int fmt, const ExpertArgs &a, bool tall) {
     const double tiles = fmax((double)a.n / h + 0.6 * a.G, fmin((double)a.n, (double)a.G));
     const double cols = ceil((double)a.N / (i == 0 ? kCols : 256));
     double rounds = fmax(fmin(tiles, (double)a.n) * cols / 256, i == 0 ? 0.0 : 1.0);
-    if (i >= 3) rounds = ceil(rounds);
+    if (i >= 3) rounds = rounds < 4 ? ceil(rounds) : rounds + 0.5;
     const double k = a.K / 2048.0, share = cost[i].share * rounds * k;
     const double t = i == 0 ? 4 + cost[i].start * k + share : cost[i].start * (i >= 3 ? rounds : 1.0) + share;
     if (t < least) {

@@ -387,9 +387,9 @@ qw_status launch_lora(LoraArgs a, hipStream_t s) {
     QW_HIP_TRY(launch(shrink_kernel<DT, MR, 2>, (unsigned)g1, kThreads, 0, s, a));
   else
     QW_HIP_TRY(launch(shrink_kernel<DT, MR, 4>, (unsigned)g1, kThreads, 0, s, a));
+  static_assert(2 * ME * 16 * (QW_MAX_RANK + 8) * 2 <= 64 * 1024, "a launch needs no attribute for its LDS");
   const size_t lds = (size_t)2 * ME * 16 * (((a.r + 31) & ~31) + 8) * 2;
   const auto expand = a.base_dtype == QW_DT_F32 ? expand_kernel<DT, ME, true> : expand_kernel<DT, ME, false>;
-  QW_HIP_TRY(hipFuncSetAttribute(reinterpret_cast<const void *>(expand), hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds));
   QW_HIP_TRY(launch(expand, (unsigned)g2, kThreads, lds, s, a));
   return QW_OK;
 }

@@ -10,6 +10,7 @@ fallback path.
 """
 
 import ctypes
+import functools
 import os
 
 import numpy as np
@@ -759,6 +760,7 @@ class Routing:
         self.ids, self.weights, self.groups = ids, weights, groups
 
 
+@functools.lru_cache(maxsize=1024)
 def qw_group_rows_workspace_bytes(n, G):
     return int(lib().qw_group_rows_workspace_bytes(int(n), int(G)))
 
@@ -778,6 +780,7 @@ def qw_group_rows(ids, G, workspace=None):
     return RowGroups(offsets, rows)
 
 
+@functools.lru_cache(maxsize=1024)
 def qw_route_workspace_bytes(T, E, top_k):
     return int(lib().qw_route_workspace_bytes(int(T), int(E), int(top_k)))
 
@@ -932,13 +935,16 @@ class Adapters:
             raise ValueError("A (count, r, K), B (count, N, r) and scale (count,) do not fit together")
         if B.device != A.device or scale.device != A.device:
             raise ValueError("A, B and scale are on different devices")
-        self.A, self.B, self.scale, self.dtype = A, B, scale, A.dtype
+        self.A, self.B, self.scale, self.dtype, self._ws = A, B, scale, A.dtype, {}
         self._c = qw_adapters(self.count, self.N, self.K, self.r, _dt(A.dtype), A.data_ptr(), B.data_ptr(),
                               scale.data_ptr())
 
 
 def qw_lora_workspace_bytes(adapters, n):
-    return int(lib().qw_lora_workspace_bytes(ctypes.byref(adapters._c), int(n)))
+    nb = adapters._ws.get(n)  # by size alone
+    if nb is None:
+        nb = adapters._ws[n] = int(lib().qw_lora_workspace_bytes(ctypes.byref(adapters._c), int(n)))
+    return nb
 
 
 def qw_lora_add(adapters, x, groups, base, out_dtype=None, out=None, workspace=None):

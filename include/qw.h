@@ -127,7 +127,9 @@ const char *qw_status_str(qw_status s);
 
 /* Kernel timing without launch gaps, for benchmarks and profilers. Arms the
  * next call of qw_select_outliers, qw_pack, qgemv_2bit, qgemv_nf4,
- * qgemv_2bit_grouped or qgemm_prefill made on the calling host thread: the
+ * qgemv_2bit_grouped, qgemm_prefill, qw_group_rows, qw_route_topk,
+ * qgemm_experts, qgemm_experts_combine or qw_lora_add made on the calling
+ * host thread: the
  * first kernel that call dispatches records start_event when it begins
  * executing, and each of its kernels records stop_event when it ends, so
  * after the call the pair brackets exactly the device execution of its

@@ -229,3 +229,50 @@ def test_one_expert_equals_the_single_matrix_calls():
         pre = qw.qgemm_prefill(p, xb, out_dtype=torch.float32)
         y = qw.qgemm_experts(ex.ew, xb, g, out_dtype=torch.float32)
         assert float((y - pre).abs().max()) <= 1e-2 * float(pre.abs().max())
+
+
+@pytest.mark.parametrize("blocks", [None, 1, 2, 4])
+def test_offsets_beyond_32_bits(blocks, tune):
+    """X of more than 4 GiB: rows near its end, by every kernel that takes it."""
+    import torch
+    if blocks:
+        tune(qw.QW_TUNE_EXPERTS_ROW_BLOCKS, blocks)
+    ex = Experts("int4", 2, 48, 8192, 0, seed=21)
+    n = 270000
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(3)
+    x = torch.randn(n, 8192, generator=gen, device="cuda", dtype=torch.bfloat16)
+    ids = torch.randint(0, 2, (n,), generator=gen, device="cuda").to(torch.int32)
+    g = qw.qw_group_rows(ids, 2)
+    Y = qw.qgemm_experts(ex.ew, x, g, out_dtype=torch.float32)
+    rows = g.rows.long()
+    off = g.offsets.cpu().numpy()
+    for e in range(2):
+        at = np.r_[off[e]:off[e] + 3, off[e + 1] - 40:off[e + 1]]
+        few = x[rows[torch.from_numpy(at).cuda()]].double().cpu().numpy()
+        y, tol = products(ex, few, np.array([0, len(at), len(at)] if e == 0 else [0, 0, len(at)]), True, torch.bfloat16)
+        assert_close(Y[torch.from_numpy(at).cuda()], y, tol, torch.float32)
+
+
+def test_experts_beyond_32_bits():
+    """Packed weights of more than 4 GiB: the last experts'."""
+    import torch
+    E, N, K = 150, 8192, 8192
+    codes = torch.randint(0, 256, (E, N, K // 2), device="cuda", dtype=torch.uint8)
+    scales = torch.rand(E, N, K // 64, device="cuda") + 0.5
+    ew = qw.ExpertWeights(qw.QW_FMT_NF4_B64, E, N, K, 0, codes, scales)
+    level = torch.from_numpy(qw.qw_nf4_levels()).double().cuda()
+    for n in (5, 40, 400):
+        x = (torch.randn(n, K, device="cuda") / 64).to(torch.bfloat16)
+        ids = torch.full((n,), E - 1, dtype=torch.int32, device="cuda")
+        ids[::3] = E - 2
+        g = qw.qw_group_rows(ids, E)
+        Y = qw.qgemm_experts(ew, x, g, out_dtype=torch.float32)
+        for e in (E - 1, E - 2):
+            q = torch.stack([codes[e] & 15, codes[e] >> 4], -1).flatten(1).long()
+            w = level[q] * scales[e].double().repeat_interleave(64, 1)
+            at = (ids[g.rows.long()] == e).nonzero()[:, 0]
+            xe = x[g.rows.long()[at]].double()
+            want, mag = xe @ w.t(), xe.abs() @ w.abs().t()
+            # K additions, the levels' (or weights') rounding to bf16
+            assert bool(((Y[at].double() - want).abs() <= (K * F32 + 2.0**-8 + F32) * mag).all())

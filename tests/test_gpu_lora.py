@@ -128,3 +128,18 @@ def test_zero_and_nonfinite_rows_stay_in_their_rows():
     assert torch.equal(out[keep], clean[keep])
     assert torch.equal(out[11], base[11])
     assert bool(torch.isnan(out[8]).all()) and not bool(torch.isfinite(out[3]).any())
+
+
+def test_offsets_beyond_32_bits():
+    """base of more than 4 GiB: its last rows, with and without an adapter."""
+    import torch
+    n, count, K, N, r = 36000, 3, 64, 32768, 8
+    ad, x, _, ids = make(n, count, K, 8, r, "f16", 31, none=0.1)
+    B = torch.randn(count, N, r, device="cuda").half()
+    ad = qw.Adapters(ad.A, B, ad.scale)
+    base = torch.randn(n, N, device="cuda")
+    g, *_ = device_groups(ids, count)
+    out = qw.qw_lora_add(ad, x, g, base, out_dtype=torch.float16)
+    for s in (slice(0, 20), slice(n - 40, n)):
+        want, tol = reference(ad, x[s], base[s], ids[s])
+        assert_close(out[s], want, tol + F32 * np.abs(want), torch.float16)
