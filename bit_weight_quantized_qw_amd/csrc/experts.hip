@@ -458,12 +458,12 @@ struct CombineArgs {
   const int32_t *ids;
   const float *weights;
   void *out;
-  int T, k, N, E, dtype;
+  int t0, k, N, E, dtype;  // t0: first token of the launch
   int col_blocks;
 };
 
 __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) {
-  const int t = blockIdx.x / a.col_blocks;
+  const int t = a.t0 + (int)(blockIdx.x / a.col_blocks);
   const int n = ((int)(blockIdx.x % a.col_blocks) * 256 + (int)threadIdx.x) * 4;
   if (n >= a.N) return;
   const bool vec = a.N % 4 == 0;
@@ -497,7 +497,7 @@ __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) {
 template <int FMT, int DT, bool ANCH>
 qw_status launch_one(const ExpertArgs &a, hipStream_t s) {
   const long long grid = most_row_tiles(a.n, a.G, kRows) * a.col_tiles;
-  if (grid >= (1ll << 31)) return QW_ERR_UNSUPPORTED;
+  if (grid > kMostBlocks) return QW_ERR_UNSUPPORTED;
   QW_HIP_TRY(launch(experts_kernel<FMT, DT, ANCH>, (unsigned)grid, kThreads, 0, s, a));
   return QW_OK;
 }
@@ -652,15 +652,19 @@ qw_status qgemm_experts_combine(const qw_experts *ew, const void *H, qw_dtype h_
   if (!aligned16(ids) || !aligned16(weights) || !aligned16(workspace)) return QW_ERR_ALIGNMENT;
   QW_TRY(current_device(nullptr));
   const int col_blocks = (a.N + 1023) / 1024;
-  if ((long long)T * col_blocks >= (1ll << 31)) return QW_ERR_UNSUPPORTED;
   a.Y = workspace;
   a.x_rows = g->n;
   a.x_div = 0;
   a.by_slot = 1;
   a.y_dtype = QW_DT_F32;
   QW_TRY(run_experts(ew, h_dtype, a, as_stream(stream)));
-  CombineArgs c{reinterpret_cast<const float *>(workspace), ids, weights, out, T, top_k, a.N, ew->E, out_dtype, col_blocks};
-  QW_HIP_TRY(launch(combine_kernel, (unsigned)(T * col_blocks), 256, 0, as_stream(stream), c));
+  // as many tokens a launch as its workgroups can be counted
+  const int most = (int)(kMostBlocks / col_blocks);
+  for (int t0 = 0; t0 < T; t0 += most) {
+    const int now = T - t0 < most ? T - t0 : most;
+    CombineArgs c{reinterpret_cast<const float *>(workspace), ids, weights, out, t0, top_k, a.N, ew->E, out_dtype, col_blocks};
+    QW_HIP_TRY(launch(combine_kernel, (unsigned)(now * col_blocks), 256, 0, as_stream(stream), c));
+  }
   return QW_OK;
 }
 

@@ -16,7 +16,7 @@ qw_status launch_tall(const GroupedArgs<ROWS, DT> &a, hipStream_t s) {
   constexpr auto kernel = prefill_w_kernel<FMT, F32, 2, 1, GroupedArgs<ROWS, DT>>;
   const size_t lds = prefill_w_lds(ROWS, 2);
   const long long grid = most_row_tiles(a.n, a.G, ROWS) * a.n_tiles;
-  if (grid >= (1ll << 31)) return QW_ERR_UNSUPPORTED;
+  if (grid > kMostBlocks) return QW_ERR_UNSUPPORTED;
   QW_HIP_TRY(hipFuncSetAttribute(reinterpret_cast<const void *>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds));
   QW_HIP_TRY(launch(kernel, (unsigned)grid, 256, lds, s, a));
   return QW_OK;

@@ -478,7 +478,7 @@ double best_level_factor(int bits) {
 template <int FMT, int DT, bool ANCH, int MR>
 qw_status launch_one(const ExpertArgs &a, hipStream_t s) {
   const long long grid = most_row_tiles(a.n, a.G, 16 * MR) * a.col_tiles;
-  if (grid >= (1ll << 31)) return QW_ERR_UNSUPPORTED;
+  if (grid > kMostBlocks) return QW_ERR_UNSUPPORTED;
   QW_HIP_TRY(launch(wide_kernel<FMT, DT, ANCH, MR>, (unsigned)grid, kThreads, 0, s, a));
   return QW_OK;
 }

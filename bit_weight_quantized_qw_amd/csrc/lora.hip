@@ -380,7 +380,7 @@ qw_status launch_lora(LoraArgs a, hipStream_t s) {
   a.cols_per_group = (int)(per < 1 ? 1 : per > 8 ? 8 : per);
   a.col_groups = (col_tiles + a.cols_per_group - 1) / a.cols_per_group;
   const long long g2 = tiles2 * a.col_groups;
-  if (g1 >= (1ll << 31) || g2 >= (1ll << 31)) return QW_ERR_UNSUPPORTED;
+  if (g1 > kMostBlocks || g2 > kMostBlocks) return QW_ERR_UNSUPPORTED;
   if (a.r <= 16)
     QW_HIP_TRY(launch(shrink_kernel<DT, MR, 1>, (unsigned)g1, kThreads, 0, s, a));
   else if (a.r <= 32)

@@ -85,6 +85,10 @@ inline long long most_row_tiles(int n, int G, int height) {
   return full < n ? full : n;
 }
 
+// Most workgroups of one launch, all of which have 256 threads here: a
+// dispatch counts its threads in 32 bits.
+constexpr long long kMostBlocks = (1ll << 24) - 1;
+
 // Validates a qw_groups view (sizes, NULLs, alignment).
 inline qw_status check_groups(const qw_groups *g) {
   if (!g || g->G < 1 || g->n < 1 || !g->offsets || !g->rows) return QW_ERR_INVALID_ARG;

@@ -572,7 +572,8 @@ size_t qw_route_workspace_bytes(int T, int E, int top_k);
  *           is -1.
  *   offsets device int32 [E+1], rows device int32 [T * top_k]: the slots
  *           t * top_k + j grouped by ids[t][j], as qw_group_rows leaves them.
- * The exponentials and their sum are fp32. 1 <= top_k <= min(E,
+ * The exponentials and their sum are fp32; a token with a +inf logit has NaN
+ * weights, as the formula gives. 1 <= top_k <= min(E,
  * QW_MAX_TOPK). Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED (E >
  * QW_MAX_GROUPS, T * top_k > QW_MAX_ROWS), HIP. */
 qw_status qw_route_topk(const void *logits, qw_dtype dtype, int T, int E,
@@ -672,8 +673,10 @@ size_t qw_lora_workspace_bytes(const qw_adapters *ad, int n);
  *   workspace device scratch of workspace_bytes >=
  *        qw_lora_workspace_bytes(ad, n): the rows' r inner values in fp32
  * A x and B (A x) accumulate in fp32, the inner values enter the second
- * product to 16 bits or better. Errors: INVALID_ARG (out overlapping base
- * with another type is not checked), ALIGNMENT, UNSUPPORTED, HIP. */
+ * product to 16 bits or better. x is finite: a row with an infinity or NaN
+ * gives values that are not, in that row alone. Errors: INVALID_ARG (out
+ * overlapping base with another type is not checked), ALIGNMENT,
+ * UNSUPPORTED, HIP. */
 qw_status qw_lora_add(const qw_adapters *ad, const void *x, const qw_groups *g,
                       const void *base, qw_dtype base_dtype, void *out,
                       qw_dtype out_dtype, void *workspace, size_t workspace_bytes,

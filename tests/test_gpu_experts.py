@@ -276,3 +276,29 @@ def test_experts_beyond_32_bits():
             want, mag = xe @ w.t(), xe.abs() @ w.abs().t()
             # K additions, the levels' (or weights') rounding to bf16
             assert bool(((Y[at].double() - want).abs() <= (K * F32 + 2.0**-8 + F32) * mag).all())
+
+
+def test_combine_of_most_tokens():
+    """More tokens than one launch has workgroups for: all of them."""
+    import torch
+    E, N, K, T = 2, 8, 64, qw.QW_MAX_ROWS
+    codes = torch.randint(0, 256, (E, N, K // 2), device="cuda", dtype=torch.uint8)
+    scales = torch.rand(E, N, K // 64, device="cuda") + 0.5
+    ew = qw.ExpertWeights(qw.QW_FMT_NF4_B64, E, N, K, 0, codes, scales)
+    level = torch.from_numpy(qw.qw_nf4_levels()).double().cuda()
+    ids = torch.randint(0, E, (T, 1), device="cuda", dtype=torch.int32)
+    weights = torch.rand(T, 1, device="cuda")
+    g = qw.qw_group_rows(ids.flatten(), E)
+    h = torch.randn(T, K, device="cuda", dtype=torch.bfloat16)  # grouped order
+    out = torch.full((T, N), 7.0, device="cuda")
+    qw.qgemm_experts_combine(ew, h, g, ids, weights, out=out)
+    at = torch.cat([torch.arange(1000), torch.randint(0, T, (20000,)), torch.arange(T - 1000, T)]).cuda()  # positions
+    t = g.rows[at].long()
+    q = torch.stack([codes & 15, codes >> 4], -1).flatten(2).long()
+    w = level[q] * scales.double()  # (E, N, K): one scale a row
+    we, x = w[ids[t, 0].long()], h[at].double()
+    want = (we * x[:, None]).sum(-1) * weights[t].double()
+    mag = (we * x[:, None]).abs().sum(-1) * weights[t].double()
+    # K additions and the weighting, the levels' (or weights') rounding to bf16
+    assert bool(((out[t].double() - want).abs() <= (K * F32 + 2.0**-8 + 3 * F32) * mag).all())
+    assert int((out == 7.0).all(1).sum()) == 0
