@@ -163,7 +163,16 @@ __global__ __launch_bounds__(256 * WM) void prefill_w_kernel(Args a) {
   // Entries lie 256 bytes apart, so that one byte permute makes an address;
   // tiles of 128 rows pack them (one more instruction) for two workgroups a CU.
   constexpr int kEntryBytes = BM > 128 ? 256 : 128;
-  __shared__ __attribute__((aligned(16))) char pair_tab[kTab ? 256 * kEntryBytes : 16];
+  constexpr int kTabBytes = kTab ? 256 * kEntryBytes : 16;
+  // fp16 operands: a column's weights enter times a power of two that brings
+  // the largest that its scales allow to 2^14..2^15, and its sums leave
+  // divided by it. fp16 by itself would hold neither a weight beyond 65504
+  // nor, to its 11 bits, one below 2^-14; so it holds those down to 2^-28 of
+  // the column's largest. bf16 has the exponents of fp32 and takes them as
+  // they are. The scales are read twice for it (8192 fp16 rows over 8 experts
+  // of 14336 x 4096 in 2-bit: 1148 us, 1072 without).
+  constexpr bool kFit = DT == QW_DT_F16;
+  __shared__ __attribute__((aligned(16))) char pair_tab[kTabBytes + (kFit ? 4 * 32 * NJ * 4 : 0)];
   const uint32_t lane_rep = 8u * (uint32_t)(threadIdx.x & 15);
 
   const int tid = threadIdx.x;
@@ -272,6 +281,44 @@ __global__ __launch_bounds__(256 * WM) void prefill_w_kernel(Args a) {
     }
   };
 
+  [[maybe_unused]] float fit[NJ];  // the columns' powers of two
+  [[maybe_unused]] float *const unfit = reinterpret_cast<float *>(pair_tab + kTabBytes) + wn * 32 * NJ;  // their inverses
+  if constexpr (kFit) {
+    // lanes l and l + 32 share a column and take its steps in turn
+    float top[NJ];
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) top[j] = 0.0f;
+#pragma unroll 8
+    for (int kt = hk; kt < KT; kt += 2) {
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        if (FMT == QW_FMT_2BIT_G32) {
+          const u32x2 sz = __builtin_amdgcn_raw_buffer_load_b64(rscale, (int)(so[j] + (uint32_t)kt * 8), 0, 0);
+#pragma unroll
+          for (int g = 0; g < 2; ++g)
+            top[j] = fmaxf(top[j], __builtin_fmaf(1.52f, fabsf(f16_bits_to_f32((uint16_t)sz[g])),
+                                                  fabsf(f16_bits_to_f32((uint16_t)(sz[g] >> 16)))));
+        } else {
+          const uint32_t s = __builtin_amdgcn_raw_buffer_load_b32(rscale, (int)(so[j] + (uint32_t)kt * 4), 0, 0);
+          if (FMT == QW_FMT_INT4_G32)
+            top[j] = fmaxf(top[j], 8.0f * fmaxf(fabsf(f16_bits_to_f32((uint16_t)s)), fabsf(f16_bits_to_f32((uint16_t)(s >> 16)))));
+          else
+            top[j] = fmaxf(top[j], fabsf(__builtin_bit_cast(float, s)));
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      const float t = fmaxf(top[j], __shfl_xor(top[j], 32, 64));
+      // 2^(14 - exponent of t), within what has a normal inverse; a column of
+      // zeros, or with an infinite scale, as it is
+      const int e = (int)(__builtin_bit_cast(uint32_t, t) >> 23) - 127;
+      const int up = t > 0.0f && e < 128 ? min(14 - e, 126) : 0;
+      fit[j] = __builtin_bit_cast(float, (uint32_t)(127 + up) << 23);
+      unfit[j * 32 + (lane & 31)] = __builtin_bit_cast(float, (uint32_t)(127 - up) << 23);
+    }
+  }
+
   floatx16 acc[IM][NJ];
 #pragma unroll
   for (int i = 0; i < IM; ++i)
@@ -299,7 +346,8 @@ __global__ __launch_bounds__(256 * WM) void prefill_w_kernel(Args a) {
       // byte q. Each nibble u becomes a float exactly (byte to float), and
       // u s - 8 s = (u - 8) s exactly (both products fit fp32), so the fma
       // gives fl32(s q) before the one rounding to bf16.
-      const float s = f16_bits_to_f32((uint16_t)(w[j][8] >> (16 * (kk >> 1))));
+      float s = f16_bits_to_f32((uint16_t)(w[j][8] >> (16 * (kk >> 1))));
+      if constexpr (kFit) s *= fit[j];
       const float ns8 = -8.0f * s;
       // the word picked with a byte permute (a select here becomes an
       // indexed read that moves the W registers to private memory)
@@ -311,7 +359,8 @@ __global__ __launch_bounds__(256 * WM) void prefill_w_kernel(Args a) {
                            __builtin_fmaf((float)((hi >> (8 * q)) & 0xFFu), s, ns8));
     } else {
       // NF4: one fp32 absmax per 64
-      const float am = __builtin_bit_cast(float, w[j][8]);
+      float am = __builtin_bit_cast(float, w[j][8]);
+      if constexpr (kFit) am *= fit[j];
       // elements kk*16 + hk*8 .. +7 = bytes 4*(2kk+hk) .. +3 of the 32 code bytes
       const uint32_t c = hk ? w[j][2 * kk + 1] : w[j][2 * kk];
 #pragma unroll
@@ -339,8 +388,12 @@ __global__ __launch_bounds__(256 * WM) void prefill_w_kernel(Args a) {
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
           const uint32_t szw = w[j][4 + g];
-          const float S = f16_bits_to_f32((uint16_t)(szw & 0xFFFFu));
-          const float Z = f16_bits_to_f32((uint16_t)(szw >> 16));
+          float S = f16_bits_to_f32((uint16_t)(szw & 0xFFFFu));
+          float Z = f16_bits_to_f32((uint16_t)(szw >> 16));
+          if constexpr (kFit) {
+            S *= fit[j];
+            Z *= fit[j];
+          }
           T[j][g][0] = pack16x2<DT>(__builtin_fmaf(S, -1.52f, Z), __builtin_fmaf(S, -0.45f, Z));
           T[j][g][1] = pack16x2<DT>(__builtin_fmaf(S, 0.45f, Z), __builtin_fmaf(S, 1.52f, Z));
         }
@@ -503,6 +556,10 @@ __global__ __launch_bounds__(256 * WM) void prefill_w_kernel(Args a) {
       for (int q = 0; q < CW; q += 4) {
         const float4 t = *reinterpret_cast<const float4 *>(slab + rr * SL + cc + q);
         v[q] = t.x; v[q + 1] = t.y; v[q + 2] = t.z; v[q + 3] = t.w;
+        if constexpr (kFit) {
+          const float4 u = *reinterpret_cast<const float4 *>(unfit + cc + q);
+          v[q] *= u.x; v[q + 1] *= u.y; v[q + 2] *= u.z; v[q + 3] *= u.w;
+        }
       }
       const uint32_t rowb = gm < y_rows ? (uint32_t)gm * a.N * esz : kPfOob;
       if (vec) {

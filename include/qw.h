@@ -611,9 +611,10 @@ typedef struct {
  * few rows per expert scale fp32 sums of exact code levels, so no weight is
  * rounded (NF4 levels are, to two numbers of x_dtype, or with more rows to
  * one after a common factor); plain products with more rows round the
- * weights to x_dtype, as qgemm_prefill does (F16: infinite beyond 65504).
- * K must be a multiple of 64
- * and N K below 2^32. No workspace.
+ * weights to x_dtype, as qgemm_prefill does (F16: after a power of two per
+ * expert and column, which keeps a weight's 11 bits from the column's
+ * largest down to 2^-28 of it, whatever their size). K must be a multiple
+ * of 64 and N K below 2^32. No workspace.
  * Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED, HIP. */
 qw_status qgemm_experts(const qw_experts *ew, const void *X, qw_dtype x_dtype,
                         int x_rows, int x_div, const qw_groups *g, int swiglu,
