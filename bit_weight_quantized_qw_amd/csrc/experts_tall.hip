@@ -54,7 +54,7 @@ qw_status launch_fmt(int fmt, const ExpertArgs &a, hipStream_t s) {
 }  // namespace
 
 bool experts_tall_fits(int x_dtype, const ExpertArgs &a) {
-  const size_t lim = 1ull << 31, esz = a.y_dtype == QW_DT_F32 ? 4 : 2;
+  const size_t lim = kPfOob, esz = a.y_dtype == QW_DT_F32 ? 4 : 2;
   return (a.y_dtype == QW_DT_F32 || a.y_dtype == x_dtype) && !a.swiglu && a.n_out == 0 &&
          (size_t)a.x_rows * a.K * 2 < lim && (size_t)a.n * a.N * esz < lim;
 }

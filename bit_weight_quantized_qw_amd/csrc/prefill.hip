@@ -354,8 +354,8 @@ int wide_column_tiles(int mt, int N, int cus) {
 template <int FMT>
 qw_status launch_fmt(const PrefillArgs &a, bool f32, int cus, hipStream_t s) {
   const size_t esz = f32 ? 4 : 2;
-  const bool fits32 = (size_t)a.M * a.K * 2 < (1ull << 31) && (size_t)a.M * a.N * esz < (1ull << 31) &&
-                      (size_t)a.N * (a.K / 2) < (1ull << 31);
+  const bool fits32 = (size_t)a.M * a.K * 2 < kPfOob && (size_t)a.M * a.N * esz < kPfOob &&
+                      (size_t)a.N * (a.K / 2) < kPfOob;
   if (a.n_out == 0 && fits32) {  // W straight to registers
     // the test hook QW_TUNE_PREFILL_WIDE_TILES overrides the number of
     // 256-wide column tiles (tests run the 128-wide kernel on small shapes)

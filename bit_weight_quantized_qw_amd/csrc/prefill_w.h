@@ -139,7 +139,9 @@ __device__ inline void xcd_tile(int b, int mt, int nt, int gmax, int &m_tile, in
 __device__ inline __amdgpu_buffer_rsrc_t pf_rsrc(const void *p, uint32_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), (short)0, (int)bytes, 0x00020000);
 }
-constexpr uint32_t kPfOob = 0x7FFFFFF0u;  // an offset always past a buffer's end
+// An offset past every buffer's end (reads 0, drops stores): callers take
+// these kernels only where X, Y and the codes are below so many bytes.
+constexpr uint32_t kPfOob = 0x80000000u;
 
 // Dynamic LDS bytes of a workgroup of four waves: two X buffers, over which
 // the epilogue's slabs lie.
