@@ -225,8 +225,7 @@ __global__ __launch_bounds__(kThreads, 3) void experts_kernel(ExpertArgs a) {
       fill_table<FMT, DT, kThreads>(tab, a);
       __syncthreads();
     }
-    if (a.x_div) xr /= a.x_div;
-    if ((uint32_t)xr >= (uint32_t)a.x_rows) xr = 0;
+    if (a.x_div) xr = max(x_row(xr, a.x_div, a.x_rows), 0);
     xp = a.X + (size_t)xr * K;
   };
 
@@ -404,7 +403,7 @@ __global__ __launch_bounds__(kThreads, 3) void experts_kernel(ExpertArgs a) {
   if (a.by_slot) {
     yr = a.rows[yr];
     if ((uint32_t)yr >= (uint32_t)a.n) return;
-  } else if (a.x_div && (uint32_t)(a.rows[yr] / a.x_div) >= (uint32_t)a.x_rows) {
+  } else if (a.x_div && x_row(a.rows[yr], a.x_div, a.x_rows) < 0) {
     return;
   }
   auto total = [&](int c) {

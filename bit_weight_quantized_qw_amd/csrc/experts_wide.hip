@@ -76,8 +76,7 @@ __global__ __launch_bounds__(kThreads, 2) void wide_kernel(ExpertArgs a) {
   for (int i = 0; i < kPieces; ++i) {
     const int row = pr + 32 * i;
     const int p = rt.p0 + (row < rt.cnt ? row : 0);
-    int xr = a.x_div ? a.rows[p] / a.x_div : p;
-    if ((uint32_t)xr >= (uint32_t)a.x_rows) xr = 0;
+    const int xr = a.x_div ? max(x_row(a.rows[p], a.x_div, a.x_rows), 0) : p;
     xp[i] = a.X + (size_t)xr * K + pc * 8;
     xat[i] = (uint32_t)row * (kStage * 2) + (uint32_t)((pc ^ (row & 7)) * 16);
   }
@@ -403,7 +402,7 @@ __global__ __launch_bounds__(kThreads, 2) void wide_kernel(ExpertArgs a) {
       if (a.by_slot) {
         yr = a.rows[yr];
         if ((uint32_t)yr >= (uint32_t)a.n) yr = -1;
-      } else if (a.x_div && (uint32_t)(a.rows[yr] / a.x_div) >= (uint32_t)a.x_rows) {
+      } else if (a.x_div && x_row(a.rows[yr], a.x_div, a.x_rows) < 0) {
         yr = -1;
       }
     }

@@ -223,7 +223,7 @@ __global__ __launch_bounds__(256 * WM) void prefill_w_kernel(Args a) {
     int gm = m0 + xr + 32 * WM * i;
     if constexpr (Args::kGrouped) {
       const int q = xr + 32 * WM * i, p = rt.p0 + q;
-      gm = q < rt.cnt ? (a.x_div ? a.rows[p] / a.x_div : p) : a.M;
+      gm = q < rt.cnt ? (a.x_div ? x_row(a.rows[p], a.x_div, a.M) : p) : a.M;
       if (gm < 0) gm = a.M;
     }
     xo[i] = gm < a.M ? (uint32_t)(((size_t)gm * K + xc) * 2) : kPfOob;
@@ -550,7 +550,7 @@ __global__ __launch_bounds__(256 * WM) void prefill_w_kernel(Args a) {
         gm = y_rows;
         if (q < rt.cnt) {
           gm = a.by_slot ? a.rows[p] : p;
-          if (gm < 0 || (!a.by_slot && a.x_div && (uint32_t)(a.rows[p] / a.x_div) >= (uint32_t)a.M)) gm = y_rows;
+          if (gm < 0 || (!a.by_slot && a.x_div && x_row(a.rows[p], a.x_div, a.M) < 0)) gm = y_rows;
         }
       }
       float v[CW];

@@ -65,6 +65,13 @@ struct RowLookup {
   __device__ int operator()(int p) const { return small ? __shfl(mine, p, 64) : rows[p]; }
 };
 
+// The row of X that row number r takes, r / x_div; -1 where r is out of range
+// (the quotient alone would take -1 for row 0).
+__device__ inline int x_row(int r, int x_div, int x_rows) {
+  const int q = r / x_div;
+  return r >= 0 && q < x_rows ? q : -1;
+}
+
 // Number of those tiles, wave-uniform; no more than ascending offsets can
 // make (what the grid was sized for), whatever the offsets are.
 __device__ inline int count_row_tiles(const int32_t *offsets, int G, int n, int height) {

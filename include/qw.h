@@ -597,7 +597,8 @@ typedef struct {
  * included):
  *   Y[p][n] = sum_k X[r(p)][k] w_hat_e[n][k],   e the group of position p,
  * for every position p of a group; r(p) = rows[p] / x_div, or r(p) = p when
- * x_div is 0 (X already in grouped order). With the slots of qw_route_topk,
+ * x_div is 0 (X already in grouped order). A position whose rows[p] is
+ * negative or whose r(p) is not below x_rows is skipped. With the slots of qw_route_topk,
  * x_div = top_k takes each slot's token. swiglu != 0: N = 2I, the gate rows
  * 0..I-1 over the up rows, and Y[p][n] = silu(g) * u as in
  * qgemv_2bit_swiglu, Y being [n][I].
