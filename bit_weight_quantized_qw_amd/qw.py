@@ -735,21 +735,49 @@ def _workspace(workspace, nbytes, device):
     return workspace
 
 
-class RowGroups:
+class _Holder:
+    """References tensors for calls that take a C view of them. The view is
+    made, and the tensors checked, when a tensor was put in another's place
+    or its storage is another one; else the last view serves."""
+
+    _tensors = ()
+    _at = None   # where the tensors of the last view lay
+    _where = ()  # their data_ptr methods
+
+    def __setattr__(self, name, value):
+        object.__setattr__(self, name, value)
+        if name in self._tensors:
+            object.__setattr__(self, "_at", None)
+
+    def view(self):
+        if [p() for p in self._where] != self._at:
+            self._c = self._make()
+            self._where = [t.data_ptr for t in (getattr(self, name) for name in self._tensors) if t is not None]
+            self._at = [p() for p in self._where]
+        return self._c
+
+
+class RowGroups(_Holder):
     """Rows grouped by the matrix they take (qw_groups): ``offsets`` int32
     (G + 1,) and ``rows`` int32 (n,) CUDA tensors, referenced, not copied."""
 
+    _tensors = ("offsets", "rows")
+
     def __init__(self, offsets, rows):
+        self.offsets, self.rows = offsets, rows
+        self.view()
+
+    def _make(self):
         import torch
+        offsets, rows = self.offsets, self.rows
         _need(offsets, torch.int32, "offsets", 1)
         _need(rows, torch.int32, "rows", 1)
         if offsets.numel() < 2 or rows.numel() < 1:
             raise ValueError("offsets has G + 1 >= 2 entries, rows n >= 1")
         if offsets.device != rows.device:
             raise ValueError("offsets and rows are on different devices")
-        self.offsets, self.rows = offsets, rows
         self.G, self.n = offsets.numel() - 1, rows.numel()
-        self._c = qw_groups(self.G, self.n, offsets.data_ptr(), rows.data_ptr())
+        return qw_groups(self.G, self.n, offsets.data_ptr(), rows.data_ptr())
 
 
 class Routing:
@@ -807,10 +835,12 @@ def qw_route_topk(logits, top_k, normalize=True, workspace=None):
     return Routing(ids, weights, RowGroups(offsets, rows))
 
 
-class ExpertWeights:
+class ExpertWeights(_Holder):
     """The packed weights of E experts of one shape, one behind another in
     each buffer (qw_experts). Buffers that are given are referenced, not
     copied; the others are allocated, uninitialised."""
+
+    _tensors = ("codes", "scales", "out_idx", "out_w", "out_mask")
 
     def __init__(self, fmt, E, N, K, n_out=0, codes=None, scales=None, out_idx=None, out_w=None, out_mask=None,
                  device="cuda"):
@@ -821,23 +851,27 @@ class ExpertWeights:
         self.format, self.E, self.N, self.K, self.n_out, self.n_out_pad = fmt, E, N, K, n_out, z["n_out_pad"]
         if fmt == QW_FMT_INT4_G32:
             z["out_idx"] = 0  # the products do not read the permutation
-        for name, given in (("codes", codes), ("scales", scales), ("out_idx", out_idx), ("out_w", out_w),
-                            ("out_mask", out_mask)):
-            nb = E * z[name]
+        self._bytes = {name: E * z[name] for name in self._tensors}
+        for name, given in zip(self._tensors, (codes, scales, out_idx, out_w, out_mask)):
+            nb = self._bytes[name]
             if nb == 0:
                 t = None
             elif given is not None:
-                _need_bytes(given, nb, name)
                 t = given
             else:
                 t = torch.empty(nb, dtype=torch.uint8, device=device)
                 t = t.view(torch.int16) if name == "out_w" else t.view(torch.int32) if name.startswith("out_") else t
             setattr(self, name, t)
-        if len({t.device for t in (self.codes, self.scales, self.out_idx, self.out_w, self.out_mask) if t is not None}) > 1:
+        self.view()
+
+    def _make(self):
+        used = {name: getattr(self, name) for name, nb in self._bytes.items() if nb}
+        for name, t in used.items():
+            _need_bytes(t, self._bytes[name], name)
+        if len({t.device for t in used.values()}) > 1:
             raise ValueError("the experts' buffers are on different devices")
-        p = lambda t: t.data_ptr() if t is not None else None
-        self._c = qw_experts(E, qw_weight(fmt, N, K, n_out, self.n_out_pad, p(self.codes), p(self.scales),
-                                          p(self.out_idx), p(self.out_w), p(self.out_mask)))
+        p = [used[name].data_ptr() if name in used else None for name in self._tensors]
+        return qw_experts(self.E, qw_weight(self.format, self.N, self.K, self.n_out, self.n_out_pad, *p))
 
     @classmethod
     def stack(cls, packed):
@@ -870,6 +904,7 @@ def qgemm_experts(ew, X, groups, top_k=1, swiglu=False, out_dtype=None, out=None
     swiglu: silu(gate) * up of merged gate/up experts. Rows of ``out`` that
     are in no group are left as they were."""
     import torch
+    w, g = ew.view(), groups.view()
     _experts_x(ew, X, "X")
     if groups.G != ew.E:
         raise ValueError(f"{groups.G} groups, {ew.E} experts")
@@ -885,8 +920,8 @@ def qgemm_experts(ew, X, groups, top_k=1, swiglu=False, out_dtype=None, out=None
     if tuple(Y.shape) != (groups.n, N):
         raise ValueError(f"output shape {tuple(Y.shape)}, expected {(groups.n, N)}")
     stream = _here(X, Y, groups.offsets, ew.codes)
-    _check(lib().qgemm_experts(ctypes.byref(ew._c), X.data_ptr(), _dt(X.dtype), X.shape[0], div,
-                               ctypes.byref(groups._c), 1 if swiglu else 0, Y.data_ptr(), _w_dtype(Y), stream),
+    _check(lib().qgemm_experts(ctypes.byref(w), X.data_ptr(), _dt(X.dtype), X.shape[0], div,
+                               ctypes.byref(g), 1 if swiglu else 0, Y.data_ptr(), _w_dtype(Y), stream),
            "qgemm_experts")
     return Y
 
@@ -900,6 +935,7 @@ def qgemm_experts_combine(ew, H, groups, ids, weights, out_dtype=None, out=None,
     e = ids[t, j]: the down projections of a routed layer, H (T * k, K) in
     grouped order, summed per token."""
     import torch
+    w, g = ew.view(), groups.view()
     _experts_x(ew, H, "H")
     _need(ids, torch.int32, "ids", 2)
     _need(weights, torch.float32, "weights", 2)
@@ -911,19 +947,26 @@ def qgemm_experts_combine(ew, H, groups, ids, weights, out_dtype=None, out=None,
         raise ValueError(f"output shape {tuple(Y.shape)}, expected {(T, ew.N)}")
     ws = _workspace(workspace, qw_experts_combine_workspace_bytes(ew.N, T, k), H.device)
     stream = _here(H, Y, ids, weights, ws, groups.offsets, ew.codes)
-    _check(lib().qgemm_experts_combine(ctypes.byref(ew._c), H.data_ptr(), _dt(H.dtype), ctypes.byref(groups._c),
+    _check(lib().qgemm_experts_combine(ctypes.byref(w), H.data_ptr(), _dt(H.dtype), ctypes.byref(g),
                                        ids.data_ptr(), weights.data_ptr(), T, k, Y.data_ptr(), _w_dtype(Y),
                                        ws.data_ptr(), ws.numel(), stream), "qgemm_experts_combine")
     return Y
 
 
-class Adapters:
+class Adapters(_Holder):
     """Low-rank adapters of one projection (qw_adapters): A (count, r, K) and
     B (count, N, r), fp16 or bf16, and scale (count,) fp32 CUDA tensors,
     referenced, not copied. Adapters of a smaller rank are padded with zeros."""
 
+    _tensors = ("A", "B", "scale")
+
     def __init__(self, A, B, scale):
+        self.A, self.B, self.scale = A, B, scale
+        self.view()
+
+    def _make(self):
         import torch
+        A, B, scale = self.A, self.B, self.scale
         if A.dtype not in (torch.float16, torch.bfloat16) or B.dtype != A.dtype:
             raise TypeError("A and B must both be fp16 or both bf16")
         _need(A, A.dtype, "A", 3)
@@ -935,15 +978,19 @@ class Adapters:
             raise ValueError("A (count, r, K), B (count, N, r) and scale (count,) do not fit together")
         if B.device != A.device or scale.device != A.device:
             raise ValueError("A, B and scale are on different devices")
-        self.A, self.B, self.scale, self.dtype, self._ws = A, B, scale, A.dtype, {}
-        self._c = qw_adapters(self.count, self.N, self.K, self.r, _dt(A.dtype), A.data_ptr(), B.data_ptr(),
-                              scale.data_ptr())
+        self.dtype, self._ws = A.dtype, {}
+        return qw_adapters(self.count, self.N, self.K, self.r, _dt(A.dtype), A.data_ptr(), B.data_ptr(),
+                           scale.data_ptr())
 
 
 def qw_lora_workspace_bytes(adapters, n):
-    nb = adapters._ws.get(n)  # by size alone
+    return _lora_workspace_bytes(adapters, adapters.view(), n)
+
+
+def _lora_workspace_bytes(adapters, view, n):
+    nb = adapters._ws.get(n)  # by sizes alone
     if nb is None:
-        nb = adapters._ws[n] = int(lib().qw_lora_workspace_bytes(ctypes.byref(adapters._c), int(n)))
+        nb = adapters._ws[n] = int(lib().qw_lora_workspace_bytes(ctypes.byref(view), int(n)))
     return nb
 
 
@@ -953,6 +1000,7 @@ def qw_lora_add(adapters, x, groups, base, out_dtype=None, out=None, workspace=N
     shared projection's output (any of the three types); out=base adds in
     place."""
     import torch
+    a, g = adapters.view(), groups.view()
     _need(x, adapters.dtype, "x", 2)
     n = x.shape[0]
     if x.shape[1] != adapters.K or tuple(base.shape) != (n, adapters.N):
@@ -962,9 +1010,9 @@ def qw_lora_add(adapters, x, groups, base, out_dtype=None, out=None, workspace=N
     Y = out if out is not None else torch.empty((n, adapters.N), dtype=out_dtype or base.dtype, device=x.device)
     if tuple(Y.shape) != (n, adapters.N):
         raise ValueError(f"output shape {tuple(Y.shape)}, expected {(n, adapters.N)}")
-    ws = _workspace(workspace, qw_lora_workspace_bytes(adapters, n), x.device)
+    ws = _workspace(workspace, _lora_workspace_bytes(adapters, a, n), x.device)
     stream = _here(x, base, Y, ws, groups.offsets, adapters.A)
-    _check(lib().qw_lora_add(ctypes.byref(adapters._c), x.data_ptr(), ctypes.byref(groups._c), base.data_ptr(),
+    _check(lib().qw_lora_add(ctypes.byref(a), x.data_ptr(), ctypes.byref(g), base.data_ptr(),
                              _w_dtype(base), Y.data_ptr(), _w_dtype(Y), ws.data_ptr(), ws.numel(), stream),
            "qw_lora_add")
     return Y
