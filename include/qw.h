@@ -513,7 +513,10 @@ qw_status qgemm_prefill(const qw_weight *w, const void *X, int M, void *Y,
  * projection. (The OTF-LLM page names neither; its per-token streaming
  * argument, section 1, is theirs too: a matrix that some row takes should
  * be read once for all rows that take it.) They share one description of
- * which row takes which matrix: the rows in the order of their matrices. */
+ * which row takes which matrix: the rows in the order of their matrices.
+ * A workspace of any of them is written and read by the call alone: calls
+ * that overlap in time, replays of captured ones among them, must not share
+ * it. */
 
 /* Largest number of groups (experts or adapters) of one call. */
 #define QW_MAX_GROUPS 1024
@@ -606,16 +609,23 @@ typedef struct {
  *      is 0); g->G == ew->E
  *   Y  device [g->n][N or I] of y_dtype F16, BF16 or F32, rounded once, not
  *      overlapping X; rows of positions in no group are left as they were.
- * Activations are finite: a row with an infinity or NaN gives values that
- * are not, in that row alone.
- * fp32 accumulation. Gated products, experts with anchors, and any with
- * few rows per expert scale fp32 sums of exact code levels, so no weight is
- * rounded (NF4 levels are, to two numbers of x_dtype, or with more rows to
- * one after a common factor); plain products with more rows round the
- * weights to x_dtype, as qgemm_prefill does (F16: after a power of two per
- * expert and column, which keeps a weight's 11 bits from the column's
- * largest down to 2^-28 of it, whatever their size). K must be a multiple
- * of 64 and N K below 2^32. No workspace.
+ * Activations are finite (a row with an infinity or NaN gives values that
+ * are not, in that row alone) and below 2^110 in size: sums of 32 of them
+ * times code levels are taken before the scale.
+ * fp32 accumulation. What is rounded before the product goes by the kernel,
+ * which is chosen by an estimate of its time from n, E, N, K and the format,
+ * so a row's last bits depend on how many rows share the call:
+ *  - few rows per expert: fp32 sums of exact code levels are scaled, no
+ *    weight is rounded (an NF4 level is two numbers of x_dtype);
+ *  - more rows, gated or with anchors (or rows or outputs of 2 GiB and
+ *    more): the same, but an NF4 level is one number of x_dtype, after a
+ *    common factor, and the sums of x that a 2-bit Z multiplies are two bf16
+ *    numbers (off by up to 2^-15 of |Z| sum |x|);
+ *  - more rows, plain: the weights are rounded to x_dtype, as qgemm_prefill
+ *    does (F16: after a power of two per expert and column, which keeps a
+ *    weight's 11 bits from the column's largest down to 2^-28 of it,
+ *    whatever their size).
+ * K must be a multiple of 64 and N K below 2^32. No workspace.
  * Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED, HIP. */
 qw_status qgemm_experts(const qw_experts *ew, const void *X, qw_dtype x_dtype,
                         int x_rows, int x_div, const qw_groups *g, int swiglu,
@@ -674,9 +684,11 @@ size_t qw_lora_workspace_bytes(const qw_adapters *ad, int n);
  *        BF16 or F32 each)
  *   workspace device scratch of workspace_bytes >=
  *        qw_lora_workspace_bytes(ad, n): the rows' r inner values in fp32
- * A x and B (A x) accumulate in fp32, the inner values enter the second
- * product to 16 bits or better. x is finite: a row with an infinity or NaN
- * gives values that are not, in that row alone. Errors: INVALID_ARG (out
+ * A x and B (A x) accumulate in fp32. The inner values enter the second
+ * product as two numbers of ad->dtype, after a power of two per row: off by
+ * up to 2^-16 of themselves (BF16), or 2^-22 of themselves and 2^-24 of the
+ * row's largest (F16). x is finite: a row with an infinity or NaN gives
+ * values that are not, in that row alone. Errors: INVALID_ARG (out
  * overlapping base with another type is not checked), ALIGNMENT,
  * UNSUPPORTED, HIP. */
 qw_status qw_lora_add(const qw_adapters *ad, const void *x, const qw_groups *g,
