@@ -735,37 +735,25 @@ def _workspace(workspace, nbytes, device):
     return workspace
 
 
-class _Holder:
-    """References tensors for calls that take a C view of them. The view is
-    made, and the tensors checked, when a tensor was put in another's place
-    or its storage is another one; else the last view serves."""
-
-    _tensors = ()
-    _at = None   # where the tensors of the last view lay
-    _where = ()  # their data_ptr methods
-
-    def __setattr__(self, name, value):
-        object.__setattr__(self, name, value)
-        if name in self._tensors:
-            object.__setattr__(self, "_at", None)
-
-    def view(self):
-        if [p() for p in self._where] != self._at:
-            self._c = self._make()
-            self._where = [t.data_ptr for t in (getattr(self, name) for name in self._tensors) if t is not None]
-            self._at = [p() for p in self._where]
-        return self._c
+# The holders below reference tensors. A call takes their C view, which is made
+# again, and the tensors checked, when a tensor was put in another's place or
+# its storage is another one (compared piece by piece: a call takes as little
+# as 10 us).
 
 
-class RowGroups(_Holder):
+class RowGroups:
     """Rows grouped by the matrix they take (qw_groups): ``offsets`` int32
     (G + 1,) and ``rows`` int32 (n,) CUDA tensors, referenced, not copied."""
 
-    _tensors = ("offsets", "rows")
-
     def __init__(self, offsets, rows):
         self.offsets, self.rows = offsets, rows
-        self.view()
+        self._c = self._make()
+
+    def view(self):
+        o, r, po, pr = self._seen
+        if o is not self.offsets or r is not self.rows or o.data_ptr() != po or r.data_ptr() != pr:
+            self._c = self._make()
+        return self._c
 
     def _make(self):
         import torch
@@ -777,7 +765,9 @@ class RowGroups(_Holder):
         if offsets.device != rows.device:
             raise ValueError("offsets and rows are on different devices")
         self.G, self.n = offsets.numel() - 1, rows.numel()
-        return qw_groups(self.G, self.n, offsets.data_ptr(), rows.data_ptr())
+        po, pr = offsets.data_ptr(), rows.data_ptr()
+        self._seen = offsets, rows, po, pr
+        return qw_groups(self.G, self.n, po, pr)
 
 
 class Routing:
@@ -835,7 +825,7 @@ def qw_route_topk(logits, top_k, normalize=True, workspace=None):
     return Routing(ids, weights, RowGroups(offsets, rows))
 
 
-class ExpertWeights(_Holder):
+class ExpertWeights:
     """The packed weights of E experts of one shape, one behind another in
     each buffer (qw_experts). Buffers that are given are referenced, not
     copied; the others are allocated, uninitialised."""
@@ -862,7 +852,15 @@ class ExpertWeights(_Holder):
                 t = torch.empty(nb, dtype=torch.uint8, device=device)
                 t = t.view(torch.int16) if name == "out_w" else t.view(torch.int32) if name.startswith("out_") else t
             setattr(self, name, t)
-        self.view()
+        self._c = self._make()
+
+    def view(self):
+        now = self.codes, self.scales, self.out_idx, self.out_w, self.out_mask
+        for t, (u, at) in zip(now, self._seen):
+            if t is not u or (u is not None and u.data_ptr() != at):
+                self._c = self._make()
+                break
+        return self._c
 
     def _make(self):
         used = {name: getattr(self, name) for name, nb in self._bytes.items() if nb}
@@ -871,6 +869,8 @@ class ExpertWeights(_Holder):
         if len({t.device for t in used.values()}) > 1:
             raise ValueError("the experts' buffers are on different devices")
         p = [used[name].data_ptr() if name in used else None for name in self._tensors]
+        now = [getattr(self, name) for name in self._tensors]
+        self._seen = [(t, None if t is None else t.data_ptr()) for t in now]
         return qw_experts(self.E, qw_weight(self.format, self.N, self.K, self.n_out, self.n_out_pad, *p))
 
     @classmethod
@@ -953,16 +953,21 @@ def qgemm_experts_combine(ew, H, groups, ids, weights, out_dtype=None, out=None,
     return Y
 
 
-class Adapters(_Holder):
+class Adapters:
     """Low-rank adapters of one projection (qw_adapters): A (count, r, K) and
     B (count, N, r), fp16 or bf16, and scale (count,) fp32 CUDA tensors,
     referenced, not copied. Adapters of a smaller rank are padded with zeros."""
 
-    _tensors = ("A", "B", "scale")
-
     def __init__(self, A, B, scale):
         self.A, self.B, self.scale = A, B, scale
-        self.view()
+        self._c = self._make()
+
+    def view(self):
+        a, b, s, pa, pb, ps = self._seen
+        if (a is not self.A or b is not self.B or s is not self.scale or a.data_ptr() != pa or b.data_ptr() != pb
+                or s.data_ptr() != ps):
+            self._c = self._make()
+        return self._c
 
     def _make(self):
         import torch
@@ -972,15 +977,16 @@ class Adapters(_Holder):
         _need(A, A.dtype, "A", 3)
         _need(B, A.dtype, "B", 3)
         _need(scale, torch.float32, "scale", 1)
-        self.count, self.r, self.K = A.shape
-        self.N = B.shape[1]
-        if B.shape[0] != self.count or B.shape[2] != self.r or scale.numel() != self.count:
+        count, r, K = A.shape
+        N = B.shape[1]
+        if tuple(B.shape) != (count, N, r) or scale.numel() != count:
             raise ValueError("A (count, r, K), B (count, N, r) and scale (count,) do not fit together")
         if B.device != A.device or scale.device != A.device:
             raise ValueError("A, B and scale are on different devices")
-        self.dtype, self._ws = A.dtype, {}
-        return qw_adapters(self.count, self.N, self.K, self.r, _dt(A.dtype), A.data_ptr(), B.data_ptr(),
-                           scale.data_ptr())
+        self.count, self.N, self.K, self.r, self.dtype, self._ws = count, N, K, r, A.dtype, {}
+        pa, pb, ps = A.data_ptr(), B.data_ptr(), scale.data_ptr()
+        self._seen = A, B, scale, pa, pb, ps
+        return qw_adapters(count, N, K, r, _dt(A.dtype), pa, pb, ps)
 
 
 def qw_lora_workspace_bytes(adapters, n):

@@ -104,3 +104,23 @@ def test_buffers_that_do_not_fit_are_refused():
     with pytest.raises(TypeError):
         qw.qgemm_experts(ex.ew, x, g)
     del keep
+
+
+def test_a_refused_buffer_leaves_the_holder_as_it_was():
+    import torch
+    f, h, ids = inputs()
+    g, *_ = device_groups(ids, COUNT)
+    x, base = h(ROWS, K), f(ROWS, N)
+    ad = qw.Adapters(h(COUNT, R, K), h(COUNT, N, R), f(COUNT))
+    want = qw.qw_lora_add(ad, x, g, base)
+    was = ad.A, ad.B, ad.scale
+    for bad in ((h(COUNT + 1, R, K + 8), was[1], was[2]), (was[0], h(COUNT, N + 8, R + 8), was[2]), (was[0], was[1], f(COUNT - 1))):
+        ad.A, ad.B, ad.scale = bad
+        with pytest.raises(ValueError):
+            qw.qw_lora_add(ad, x, g, base)
+        ad.A, ad.B, ad.scale = was
+        assert torch.equal(qw.qw_lora_add(ad, x, g, base), want)
+    # adapters of another rank and number are taken as a whole
+    ad.A, ad.B, ad.scale = h(COUNT + 2, 2 * R, K), h(COUNT + 2, N, 2 * R), f(COUNT + 2)
+    g, *_ = device_groups(ids, COUNT + 2)
+    assert torch.equal(qw.qw_lora_add(ad, x, g, base), qw.qw_lora_add(qw.Adapters(ad.A, ad.B, ad.scale), x, g, base))
