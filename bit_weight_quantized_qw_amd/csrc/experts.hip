@@ -25,10 +25,10 @@
 // read. Lane l reads replica l % 16 of the table, so no two of 16 lanes meet
 // in a bank. Up to four rows, four scale groups share one result (below).
 //
-// Measured: 40 tokens, 2 of 16 experts of 8192 x 4096, in NF4 73 to 80 us
-// (3.8 to 4.2 TB/s), in 2-bit 69 us (2.9 TB/s), in INT4 92 us (3.3 TB/s; the
-// INT4 variant without anchors keeps 8 registers in memory); 136 slots over
-// 64 experts of 2048 x 1408 in 2-bit with anchors 28 us, 2.8 TB/s; one token's 8 of 64 experts of 2816 x 2048 12 us,
+// Measured: 40 tokens, 2 of 16 experts of 8192 x 4096, in NF4 73 to 88 us
+// (3.4 to 4.2 TB/s), in 2-bit 69 us (2.9 TB/s; INT4 takes wide tiles of 32
+// rows there, 92 us); 136 slots over 64 experts of 2048 x 1408 in 2-bit with
+// anchors 29 us, 2.7 TB/s; one token's 8 of 64 experts of 2816 x 2048 12 us,
 // of which 9 are one workgroup: 1 until its tile is known, 4 until its first
 // codes are there, 1.3 a chunk of 256 weights, 0.5 for the sums.
 //

