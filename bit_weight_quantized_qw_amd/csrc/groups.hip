@@ -22,6 +22,7 @@
 // 2^24 rows by 1024 ids take 12 ms.
 #include <math.h>
 
+#include "op16.h"
 #include "row_groups.h"
 
 namespace qw {
@@ -179,6 +180,148 @@ __device__ inline void topk_tokens(const RouteArgs &a, int t0, int count, int32_
   }
 }
 
+// ---- scores, bias and groups ---------------------------------------------
+//
+// The choice of qw_route_scored. A token's lanes are dealt to its groups of
+// experts: with the number of groups rounded up to a power of two, lane `sub`
+// belongs to group sub / P and holds the experts sub % P, sub % P + P, ... of
+// it, so a group's largest and second come from log2 P exchanges, and with
+// one group the layout is that of the top-k above. Choices are 64-bit
+// numbers: sigmoids of logits that differ in fp32 agree in fp32 as soon as
+// they come near 1, and a bias of 0.1 leaves scores of 1e-4 three digits. Each
+// round takes the largest choice (its pattern as an ordered integer) and then
+// the lowest expert that has it. The chosen experts' scores are computed again
+// from their logits, one a lane, rather than kept.
+
+struct ScoredArgs {
+  const void *logits;
+  const float *bias;
+  int32_t *ids;
+  float *weights;
+  float scale;
+  int T, E, k, normalize;
+  int score, by;
+  int groups, top_groups, group_size;
+};
+
+// Integer with the order of the number; NaN and -inf give 0.
+__device__ inline unsigned long long ordered64(double f) {
+  if (!(f > -INFINITY)) return 0ull;
+  const unsigned long long u = __builtin_bit_cast(unsigned long long, f + 0.0);  // -0 counts as 0
+  return (u >> 63) ? ~u : (u | (1ull << 63));
+}
+__device__ inline double from_ordered64(unsigned long long k) {
+  return __builtin_bit_cast(double, (k >> 63) ? (k & ~(1ull << 63)) : ~k);
+}
+
+template <int DT>
+__device__ inline float logit_at(const void *p, size_t i) {
+  if constexpr (DT == QW_DT_F32) return reinterpret_cast<const float *>(p)[i];
+  const uint32_t h = reinterpret_cast<const uint16_t *>(p)[i];
+  return DT == QW_DT_BF16 ? __builtin_bit_cast(float, h << 16) : f16_bits_to_f32((uint16_t)h);
+}
+
+template <int DT, int L, int V>
+__device__ inline void choose_tokens(const ScoredArgs &a, int t0, int count, int32_t *sid) {
+  typedef unsigned long long key_t;
+  const int sub = threadIdx.x % L;
+  int P = L;  // lanes of a group
+  while (L / P < a.groups) P /= 2;
+  const int group = sub / P;
+  for (int i = threadIdx.x / L; i < count; i += kThreads / L) {
+    const int t = t0 + i;
+    float x[V];
+    float most = -INFINITY;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int in = v * P + sub % P;
+      x[v] = -INFINITY;
+      if (group < a.groups && in < a.group_size) {
+        const float l = logit_at<DT>(a.logits, (size_t)t * a.E + group * a.group_size + in);
+        if (l > -INFINITY) x[v] = l;  // NaN is taken as -inf
+      }
+      most = fmaxf(most, x[v]);
+    }
+    double sum = 1.0;
+    if (a.score == QW_ROUTE_SOFTMAX) {
+#pragma unroll
+      for (int d = L / 2; d; d >>= 1) most = fmaxf(most, __shfl_xor(most, d, L));
+      sum = 0.0;
+#pragma unroll
+      for (int v = 0; v < V; ++v) sum += x[v] > -INFINITY ? exp((double)x[v] - (double)most) : 0.0;
+#pragma unroll
+      for (int d = L / 2; d; d >>= 1) sum += __shfl_xor(sum, d, L);
+    }
+    auto score_of = [&](float l) {
+      return a.score == QW_ROUTE_SOFTMAX ? exp((double)l - (double)most) / sum : 1.0 / (1.0 + exp(-(double)l));
+    };
+    key_t key[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      key[v] = 0;
+      if (x[v] > -INFINITY) {
+        const double bias = a.bias ? (double)a.bias[group * a.group_size + v * P + sub % P] : 0.0;
+        key[v] = ordered64(score_of(x[v]) + bias);
+      }
+    }
+    if (a.top_groups < a.groups) {
+      key_t first = 0, second = 0;  // of the group's choices
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        second = max(second, min(first, key[v]));
+        first = max(first, key[v]);
+      }
+      for (int d = P / 2; d; d >>= 1) {
+        const key_t f = __shfl_xor(first, d, L), s = __shfl_xor(second, d, L);
+        second = max(min(first, f), max(second, s));
+        first = max(first, f);
+      }
+      key_t value = first;
+      if (a.by == QW_GROUP_TOP2 && second) value = ordered64(from_ordered64(first) + from_ordered64(second));
+      int before = 0;  // groups of a larger value, or an equal one and a lower number
+      for (int g = 0; g < a.groups; ++g) {
+        const key_t o = __shfl(value, g * P, L);
+        before += o > value || (o == value && g < group);
+      }
+      if (before >= a.top_groups) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) key[v] = 0;
+      }
+    }
+    int id = -1;  // lane j of the token keeps choice j
+    for (int j = 0; j < a.k; ++j) {
+      key_t best = key[0];
+#pragma unroll
+      for (int v = 1; v < V; ++v) best = key[v] > best ? key[v] : best;
+      best = lanes_max<L>(best);
+      uint32_t at = 0;  // the inverted number of the lowest expert that has it
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        if (best && key[v] == best) at = max(at, ~(uint32_t)(group * a.group_size + v * P + sub % P));
+      at = lanes_max<L>(at);
+      if (sub == j && best) id = (int)~at;
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        if (~(uint32_t)(group * a.group_size + v * P + sub % P) == at) key[v] = 0;
+    }
+    double w = 0.0;
+    if (id >= 0) w = score_of(logit_at<DT>(a.logits, (size_t)t * a.E + id));
+    double factor = (double)a.scale;
+    if (a.normalize) {
+      double total = w;
+#pragma unroll
+      for (int d = L / 2; d; d >>= 1) total += __shfl_xor(total, d, L);
+      factor = total > 0.0 ? factor / total : 0.0;
+    }
+    if (sub < a.k) {
+      const size_t o = (size_t)t * a.k + sub;
+      a.ids[o] = id;
+      a.weights[o] = id >= 0 ? (float)(w * factor) : 0.0f;
+      if (sid) sid[i * a.k + sub] = id;
+    }
+  }
+}
+
 // ---- grouping ------------------------------------------------------------
 
 // LDS of one block: the slots' ids, the running base of every group (one
@@ -313,6 +456,21 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a, GroupArgs 
     write_counts(g, l, count * a.k);
 }
 
+template <int DT, int L, int V>
+__global__ __launch_bounds__(kThreads) void scored_kernel(ScoredArgs a, GroupArgs g) {
+  extern __shared__ int32_t smem[];
+  const GroupLds l = group_lds(smem, g.G);
+  const int tokens = g.per / a.k;  // per is a multiple of k
+  const int t0 = blockIdx.x * tokens;
+  const int count = min(tokens, a.T - t0);
+  choose_tokens<DT, L, V>(a, t0, count, l.sid);
+  __syncthreads();
+  if (g.blocks == 1)
+    group_alone(g, l);
+  else
+    write_counts(g, l, count * a.k);
+}
+
 // First launch of qw_group_rows: everything for one block, else its counts.
 __global__ __launch_bounds__(kThreads) void group_kernel(GroupArgs g) {
   extern __shared__ int32_t smem[];
@@ -394,13 +552,30 @@ int topk_lanes(int E, int k) {
 // and the top-k takes few passes; else two passes of the top-k a block (16384
 // tokens of 8 in 128: 10 us, 17 with twice as many), more where there would
 // be over 256 blocks, at most kSlots. A multiple of k.
-int block_slots(int T, int E, int k) {
-  const int pass = kThreads / topk_lanes(E, k);
+int block_slots_of(int T, int k, int lanes) {
+  const int pass = kThreads / lanes;
   if (T <= 4 * pass && (long long)T * k <= kSlots) return T * k;
   long long tokens = 2 * pass;
   while (2 * tokens * k <= kSlots && T > tokens * 256) tokens *= 2;
   while (tokens > 1 && tokens * k > kSlots) tokens /= 2;
   return (int)(tokens * k);
+}
+
+int block_slots(int T, int E, int k) { return block_slots_of(T, k, topk_lanes(E, k)); }
+
+// Lanes a token takes in the choice by scores, and the experts that a lane
+// holds: as in the top-k, with a lane at least for every group.
+int scored_lanes(int E, int k, int groups) {
+  int lanes = topk_lanes(E, k);
+  lanes = lanes < 16 ? 16 : lanes;
+  while (lanes < groups) lanes *= 2;
+  return lanes;
+}
+int scored_held(int E, int groups, int lanes) {
+  int per = lanes;  // lanes of a group
+  while (lanes / per < groups) per /= 2;
+  const int held = (E / groups + per - 1) / per;
+  return held <= 4 ? 4 : held <= 8 ? 8 : held <= 16 ? 16 : 32;
 }
 
 size_t counts_bytes(long long n, int per, int G) {
@@ -429,6 +604,29 @@ qw_status launch_route(const RouteArgs &a, const GroupArgs &g, hipStream_t s) {
   QW_ROUTE(64, 8)
   QW_ROUTE(64, 16)
 #undef QW_ROUTE
+  return QW_ERR_UNSUPPORTED;
+}
+
+template <int DT>
+qw_status launch_scored(const ScoredArgs &a, const GroupArgs &g, hipStream_t s) {
+  const size_t lds = group_lds_bytes(g.G);
+  const int lanes = scored_lanes(a.E, a.k, a.groups), held = scored_held(a.E, a.groups, lanes);
+#define QW_SCORED(L, V)                                                            \
+  if (lanes == (L) && held == (V)) {                                               \
+    QW_HIP_TRY(launch(scored_kernel<DT, L, V>, g.blocks, kThreads, lds, s, a, g)); \
+    return launch_place(g, s);                                                     \
+  }
+  QW_SCORED(16, 4)
+  QW_SCORED(16, 8)
+  QW_SCORED(16, 16)
+  QW_SCORED(32, 4)
+  QW_SCORED(32, 8)
+  QW_SCORED(32, 16)
+  QW_SCORED(64, 4)
+  QW_SCORED(64, 8)
+  QW_SCORED(64, 16)
+  QW_SCORED(64, 32)
+#undef QW_SCORED
   return QW_ERR_UNSUPPORTED;
 }
 
@@ -503,6 +701,50 @@ qw_status qw_route_topk(const void *logits, qw_dtype dtype, int T, int E, int to
   if (dtype == QW_DT_F32) return launch_route<QW_DT_F32>(a, g, as_stream(stream));
   if (dtype == QW_DT_BF16) return launch_route<QW_DT_BF16>(a, g, as_stream(stream));
   return launch_route<QW_DT_F16>(a, g, as_stream(stream));
+}
+
+size_t qw_route_scored_workspace_bytes(int T, int E, int top_k, int n_groups) {
+  if (T < 1 || E < 1 || E > QW_MAX_GROUPS || top_k < 1 || top_k > E || top_k > QW_MAX_TOPK) return 0;
+  if (n_groups < 1 || n_groups > QW_MAX_EXPERT_GROUPS || E % n_groups) return 0;
+  const long long n = (long long)T * top_k;
+  return n <= QW_MAX_ROWS ? qw::counts_bytes(n, qw::block_slots_of(T, top_k, qw::scored_lanes(E, top_k, n_groups)), E) : 0;
+}
+
+qw_status qw_route_scored(const void *logits, qw_dtype dtype, int T, int E, int top_k, qw_route_score score,
+                          const float *bias, int n_groups, int top_groups, qw_group_value group_by, int normalize,
+                          float scale, int32_t *ids, float *weights, int32_t *offsets, int32_t *rows,
+                          void *workspace, size_t workspace_bytes, void *stream) {
+  using namespace qw;
+  CallScope scope;
+  if (!logits || !ids || !weights || !offsets || !rows || T < 1 || E < 1) return QW_ERR_INVALID_ARG;
+  if (top_k < 1 || top_k > QW_MAX_TOPK || !is_dtype(dtype)) return QW_ERR_INVALID_ARG;
+  if (score != QW_ROUTE_SOFTMAX && score != QW_ROUTE_SIGMOID) return QW_ERR_INVALID_ARG;
+  if (group_by != QW_GROUP_MAX && group_by != QW_GROUP_TOP2) return QW_ERR_INVALID_ARG;
+  if (n_groups < 1 || n_groups > QW_MAX_EXPERT_GROUPS || E % n_groups) return QW_ERR_INVALID_ARG;
+  if (top_groups < 1 || top_groups > n_groups) return QW_ERR_INVALID_ARG;
+  if (top_k > E / n_groups * top_groups || !(fabsf(scale) < INFINITY)) return QW_ERR_INVALID_ARG;
+  const long long n = (long long)T * top_k;
+  if (E > QW_MAX_GROUPS || n > QW_MAX_ROWS) return QW_ERR_UNSUPPORTED;
+  const int per = block_slots_of(T, top_k, scored_lanes(E, top_k, n_groups));
+  const size_t need = counts_bytes(n, per, E);
+  if (need && (!workspace || workspace_bytes < need)) return QW_ERR_INVALID_ARG;
+  if (!aligned16(logits) || !aligned16(bias) || !aligned16(ids) || !aligned16(weights) || !aligned16(offsets) ||
+      !aligned16(rows) || (need && !aligned16(workspace)))
+    return QW_ERR_ALIGNMENT;
+  QW_TRY(current_device(nullptr));
+  ScoredArgs a{logits, bias, ids, weights, scale, T, E, top_k, normalize != 0, (int)score, (int)group_by, n_groups, top_groups, E / n_groups};
+  GroupArgs g{};
+  g.ids = ids;
+  g.offsets = offsets;
+  g.rows = rows;
+  g.counts = reinterpret_cast<int32_t *>(workspace);
+  g.n = (int)n;
+  g.G = E;
+  g.per = per;
+  g.blocks = (int)((n + per - 1) / per);
+  if (dtype == QW_DT_F32) return launch_scored<QW_DT_F32>(a, g, as_stream(stream));
+  if (dtype == QW_DT_BF16) return launch_scored<QW_DT_BF16>(a, g, as_stream(stream));
+  return launch_scored<QW_DT_F16>(a, g, as_stream(stream));
 }
 
 }  // extern "C"

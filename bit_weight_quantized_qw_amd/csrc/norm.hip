@@ -1,0 +1,299 @@
+// The root-mean-square norm before a projection, with the residual stream's
+// addition and the output in the form that the products take:
+//   h[m][k] = x[m][k] + residual[m][k]
+//   y[m][k] = h[m][k] / sqrt(mean_k h[m][k]^2 + eps) * weight[k]
+// in 16 or 32 bits, or in 8 bits with one scale a row, optionally in the
+// channel order of the INT4 format.
+//
+// What bounds it: memory, every element read once and written once. So a row
+// stays in registers between its sums and its output, held by as many waves
+// as that takes, and all of a lane's loads are requested before the first is
+// used. h is fp32 in registers: what is normalised is the unrounded sum.
+//
+// The row's sum of squares and (8 bits) the largest |h weight| come from one
+// pass and one exchange: the scale of a row is the largest y over the largest
+// number of the type, and y is h weight times one factor a row.
+#include <math.h>
+
+#include "op16.h"
+
+namespace qw {
+namespace {
+
+struct NormArgs {
+  const void *x, *residual, *weight;
+  const int32_t *perm;
+  void *h_out, *y;
+  float *y_scales;
+  float eps;
+  int M, K;
+  int x_dtype, r_dtype, w_dtype, y_dtype;
+};
+
+__device__ inline float value16(uint32_t b, int dt) {
+  return dt == QW_DT_F16 ? Op<QW_DT_F16>::value(b & 0xFFFFu) : Op<QW_DT_BF16>::value(b & 0xFFFFu);
+}
+
+// V elements as they lie in memory, S bytes each.
+template <int S, int V>
+struct Raw {
+  uint32_t w[S * V >= 4 ? S * V / 4 : 1];
+};
+
+template <int S, int V>
+__device__ inline void load_raw(Raw<S, V> &d, const void *p, size_t i) {
+  const char *at = reinterpret_cast<const char *>(p) + i * S;
+  if constexpr (S * V >= 16) {
+#pragma unroll
+    for (int q = 0; q < S * V / 16; ++q) {
+      const u32x4 v = reinterpret_cast<const u32x4 *>(at)[q];
+      d.w[4 * q] = v[0]; d.w[4 * q + 1] = v[1]; d.w[4 * q + 2] = v[2]; d.w[4 * q + 3] = v[3];
+    }
+  } else if constexpr (S * V == 4) {
+    d.w[0] = *reinterpret_cast<const uint32_t *>(at);
+  } else {
+    d.w[0] = *reinterpret_cast<const uint16_t *>(at);
+  }
+}
+
+template <int S, int V>
+__device__ inline float raw_value(const Raw<S, V> &d, int q, int dt) {
+  if constexpr (S == 4) return __builtin_bit_cast(float, d.w[q]);
+  return value16(d.w[q / 2] >> (16 * (q & 1)), dt);
+}
+
+// Stores V values at element i, rounded to dt.
+template <int V>
+__device__ inline void store_values(void *p, size_t i, const float (&v)[V], int dt) {
+  if (dt == QW_DT_F32) {
+    float *o = reinterpret_cast<float *>(p) + i;
+    if constexpr (V == 8) {
+      reinterpret_cast<f32x4 *>(o)[0] = f32x4{v[0], v[1], v[2], v[3]};
+      reinterpret_cast<f32x4 *>(o)[1] = f32x4{v[4], v[5], v[6], v[7]};
+    } else {
+      o[0] = v[0];
+    }
+    return;
+  }
+  uint16_t *o = reinterpret_cast<uint16_t *>(p) + i;
+  if constexpr (V == 8) {
+    u32x4 w;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) w[q] = out_bits(v[2 * q], dt) | (out_bits(v[2 * q + 1], dt) << 16);
+    *reinterpret_cast<u32x4 *>(o) = w;
+  } else {
+    o[0] = (uint16_t)out_bits(v[0], dt);
+  }
+}
+
+// The same in 8 bits; the values are within the type's range but for a
+// rounding of the scale's inverse.
+template <int V>
+__device__ inline void store_8bit(void *p, size_t i, const float (&v)[V], int dt) {
+  uint32_t w[V == 8 ? 2 : 1] = {0};
+  if (dt == QW_DT_I8) {
+#pragma unroll
+    for (int q = 0; q < V; ++q) {
+      const int n = (int)rintf(__builtin_amdgcn_fmed3f(v[q], -127.0f, 127.0f));
+      w[q / 4] |= ((uint32_t)n & 0xFFu) << (8 * (q & 3));
+    }
+  } else {
+    float c[V];
+#pragma unroll
+    for (int q = 0; q < V; ++q) c[q] = __builtin_amdgcn_fmed3f(v[q], -448.0f, 448.0f);
+    if constexpr (V == 8) {
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        w[q] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c[4 * q], c[4 * q + 1], 0, false);
+        w[q] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c[4 * q + 2], c[4 * q + 3], (int)w[q], true);
+      }
+    } else {
+      w[0] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c[0], 0.0f, 0, false);
+    }
+  }
+  uint8_t *o = reinterpret_cast<uint8_t *>(p) + i;
+  if constexpr (V == 8)
+    *reinterpret_cast<u32x2 *>(o) = u32x2{w[0], w[1]};
+  else
+    o[0] = (uint8_t)w[0];
+}
+
+// The smallest scale of a row: its inverse is finite, and rows of zeros (or of
+// less than 2^-100 of the type's range) give zeros.
+constexpr float kLeastScale = 0x1p-100f;
+
+// XS, RS: bytes of an element of x and of the residual (0: none); W: waves of
+// a row; IT: runs of V elements that a lane holds, at most. V is 8, or 1
+// where rows do not start on 16 bytes.
+template <int XS, int RS, int W, int IT, int V>
+__global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void norm_kernel(NormArgs a) {
+  constexpr int kRows = W == 1 ? 4 : 1;  // rows of a workgroup
+  constexpr int kLanes = 64 * W;         // lanes of a row
+  extern __shared__ float smem[];        // [kRows][K] with perm
+  __shared__ float sums[W];
+  __shared__ uint32_t tops[W];
+  const int row_of = W == 1 ? (int)threadIdx.x >> 6 : 0;
+  const int m = (int)blockIdx.x * kRows + row_of;
+  if (m >= a.M) return;  // W == 1: whole waves, and no barrier below
+  const int at = W == 1 ? (int)threadIdx.x & 63 : (int)threadIdx.x;
+  const int K = a.K;
+  const size_t row = (size_t)m * K;
+
+  Raw<XS, V> xv[IT];
+  Raw<RS ? RS : 2, V> rv[RS ? IT : 1];
+#pragma unroll
+  for (int i = 0; i < IT; ++i) {
+    const int k = (i * kLanes + at) * V;
+    if (k < K) load_raw(xv[i], a.x, row + k);
+    if constexpr (RS != 0)
+      if (k < K) load_raw(rv[i], a.residual, row + k);
+  }
+  float h[IT][V];  // then h weight
+  float sum = 0.0f;
+  uint32_t top = 0;  // |h weight| as an integer: NaN above infinity above all others
+#pragma unroll
+  for (int i = 0; i < IT; ++i) {
+    const int k = (i * kLanes + at) * V;
+    if (k >= K) continue;
+#pragma unroll
+    for (int q = 0; q < V; ++q) {
+      h[i][q] = raw_value(xv[i], q, a.x_dtype);
+      if constexpr (RS != 0) h[i][q] += raw_value(rv[i], q, a.r_dtype);
+      sum = __builtin_fmaf(h[i][q], h[i][q], sum);
+    }
+    if (RS != 0 && a.h_out) store_values<V>(a.h_out, row + k, h[i], a.r_dtype);
+    if (a.w_dtype == QW_DT_F32) {
+      Raw<4, V> g;
+      load_raw(g, a.weight, k);
+#pragma unroll
+      for (int q = 0; q < V; ++q) h[i][q] *= raw_value(g, q, a.w_dtype);
+    } else {
+      Raw<2, V> g;
+      load_raw(g, a.weight, k);
+#pragma unroll
+      for (int q = 0; q < V; ++q) h[i][q] *= raw_value(g, q, a.w_dtype);
+    }
+#pragma unroll
+    for (int q = 0; q < V; ++q) top = max(top, __builtin_bit_cast(uint32_t, h[i][q]) & 0x7FFFFFFFu);
+    if (a.perm) {
+#pragma unroll
+      for (int q = 0; q < V; ++q) smem[(size_t)row_of * K + k + q] = h[i][q];
+    }
+  }
+#pragma unroll
+  for (int d = 32; d; d >>= 1) {
+    sum += __shfl_xor(sum, d, 64);
+    top = max(top, (uint32_t)__shfl_xor((int)top, d, 64));
+  }
+  if constexpr (W > 1) {
+    const int wv = threadIdx.x >> 6;
+    if ((threadIdx.x & 63) == 0) {
+      sums[wv] = sum;
+      tops[wv] = top;
+    }
+    __syncthreads();
+    sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      sum += sums[w];
+      top = max(top, tops[w]);
+    }
+  } else {
+    // the row's LDS is written and read by one wave
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+  }
+  float f = 1.0f / sqrtf(sum / (float)K + a.eps);
+  const bool in8 = a.y_dtype == QW_DT_E4M3 || a.y_dtype == QW_DT_I8;
+  if (in8) {
+    const float most = a.y_dtype == QW_DT_I8 ? 127.0f : 448.0f;
+    const float largest = __builtin_bit_cast(float, top) * f;
+    // a row with an infinity or a NaN has no scale
+    const float scale = largest < INFINITY ? fmaxf(largest / most, kLeastScale) : NAN;
+    if (at == 0) a.y_scales[m] = scale;
+    f = largest < INFINITY ? f / scale : 0.0f;
+  }
+#pragma unroll
+  for (int i = 0; i < IT; ++i) {
+    const int k = (i * kLanes + at) * V;
+    if (k >= K) continue;
+    float v[V];
+    if (a.perm) {
+      Raw<4, V> from;
+      load_raw(from, a.perm, k);
+#pragma unroll
+      for (int q = 0; q < V; ++q) v[q] = from.w[q] < (uint32_t)K ? smem[(size_t)row_of * K + from.w[q]] * f : 0.0f;
+    } else {
+#pragma unroll
+      for (int q = 0; q < V; ++q) v[q] = h[i][q] * f;
+    }
+    if (in8) {
+      if (f == 0.0f) {  // infinity times zero is not zero
+#pragma unroll
+        for (int q = 0; q < V; ++q) v[q] = 0.0f;
+      }
+      store_8bit<V>(a.y, row + k, v, a.y_dtype);
+    } else {
+      store_values<V>(a.y, row + k, v, a.y_dtype);
+    }
+  }
+}
+
+template <int XS, int RS, int W, int IT, int V>
+qw_status launch_one(const NormArgs &a, hipStream_t s) {
+  constexpr auto kernel = norm_kernel<XS, RS, W, IT, V>;
+  constexpr int kRows = W == 1 ? 4 : 1;
+  const size_t lds = a.perm ? (size_t)kRows * a.K * sizeof(float) : 0;
+  if (lds > 32768)
+    QW_HIP_TRY(hipFuncSetAttribute(reinterpret_cast<const void *>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds));
+  QW_HIP_TRY(launch(kernel, (unsigned)((a.M + kRows - 1) / kRows), W == 1 ? 256 : 64 * W, lds, s, a));
+  return QW_OK;
+}
+
+template <int XS, int RS>
+qw_status launch_sizes(const NormArgs &a, hipStream_t s) {
+  const int K = a.K;
+  if (K % 8 == 0) {
+    if (K <= 512) return launch_one<XS, RS, 1, 1, 8>(a, s);
+    if (K <= 2048) return launch_one<XS, RS, 1, 4, 8>(a, s);
+    if (K <= 4096) return launch_one<XS, RS, 4, 2, 8>(a, s);
+    if (K <= 8192) return launch_one<XS, RS, 4, 4, 8>(a, s);
+    if (K <= 16384) return launch_one<XS, RS, 16, 2, 8>(a, s);
+    return launch_one<XS, RS, 16, 4, 8>(a, s);
+  }
+  if (K <= 512) return launch_one<XS, RS, 1, 8, 1>(a, s);
+  if (K <= 8192) return launch_one<XS, RS, 4, 32, 1>(a, s);
+  return launch_one<XS, RS, 16, 32, 1>(a, s);
+}
+
+template <int XS>
+qw_status launch_residual(const NormArgs &a, hipStream_t s) {
+  if (!a.residual) return launch_sizes<XS, 0>(a, s);
+  return a.r_dtype == QW_DT_F32 ? launch_sizes<XS, 4>(a, s) : launch_sizes<XS, 2>(a, s);
+}
+
+}  // namespace
+}  // namespace qw
+
+extern "C" qw_status qw_rmsnorm(const void *x, qw_dtype x_dtype, const void *residual, qw_dtype residual_dtype,
+                                const void *weight, qw_dtype weight_dtype, float eps, int M, int K,
+                                const int32_t *perm, void *residual_out, void *y, qw_dtype y_dtype,
+                                float *y_scales, void *stream) {
+  using namespace qw;
+  CallScope scope;
+  if (!x || !weight || !y || M < 1 || K < 1) return QW_ERR_INVALID_ARG;
+  if (!is_dtype(x_dtype) || !is_dtype(weight_dtype)) return QW_ERR_INVALID_ARG;
+  if (residual ? !is_dtype(residual_dtype) : residual_out != nullptr) return QW_ERR_INVALID_ARG;
+  const bool in8 = y_dtype == QW_DT_E4M3 || y_dtype == QW_DT_I8;
+  if (!in8 && !is_dtype(y_dtype)) return QW_ERR_INVALID_ARG;
+  if (in8 != (y_scales != nullptr)) return QW_ERR_INVALID_ARG;
+  if (!(eps >= 0.0f) || !(eps < INFINITY)) return QW_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(residual) || !aligned16(weight) || !aligned16(perm) || !aligned16(residual_out) ||
+      !aligned16(y) || !aligned16(y_scales))
+    return QW_ERR_ALIGNMENT;
+  if (K > QW_MAX_NORM_K || M > QW_MAX_ROWS) return QW_ERR_UNSUPPORTED;
+  QW_TRY(current_device(nullptr));
+  const NormArgs a{x, residual, weight, perm, residual_out, y, y_scales, eps, M, K, x_dtype, residual_dtype, weight_dtype, y_dtype};
+  return x_dtype == QW_DT_F32 ? launch_residual<4>(a, as_stream(stream)) : launch_residual<2>(a, as_stream(stream));
+}

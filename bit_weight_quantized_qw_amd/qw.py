@@ -22,9 +22,13 @@ QW_OK, QW_ERR_INVALID_ARG, QW_ERR_ALIGNMENT, QW_ERR_UNSUPPORTED, QW_ERR_HIP, QW_
 QW_ERR_SCRATCH_LIMIT = 6
 QW_STATIC_SCRATCH_BYTES = 8 << 20
 QW_FMT_2BIT_G32, QW_FMT_NF4_B64, QW_FMT_INT4_G32 = 1, 2, 3
-QW_DT_F16, QW_DT_BF16, QW_DT_F32 = 1, 2, 3
+QW_DT_F16, QW_DT_BF16, QW_DT_F32, QW_DT_E4M3, QW_DT_I8 = 1, 2, 3, 4, 5
 QW_SCORE_MEANABS, QW_SCORE_L2 = 1, 2
 QW_MAX_GROUPS, QW_MAX_TOPK, QW_MAX_ROWS, QW_MAX_RANK = 1024, 32, 1 << 24, 256
+QW_ROUTE_SOFTMAX, QW_ROUTE_SIGMOID = 1, 2
+QW_GROUP_MAX, QW_GROUP_TOP2 = 1, 2
+QW_MAX_EXPERT_GROUPS, QW_MAX_NORM_K = 64, 32768
+QW_ACT_NONE, QW_ACT_RELU, QW_ACT_SILU, QW_ACT_GELU, QW_ACT_GELU_TANH = range(5)
 
 # every function declared in include/qw.h and include/qw_tuning.h
 EXPORTS = [
@@ -39,6 +43,7 @@ EXPORTS = [
     "qw_group_rows_workspace_bytes", "qw_group_rows", "qw_route_workspace_bytes", "qw_route_topk",
     "qgemm_experts", "qw_experts_combine_workspace_bytes", "qgemm_experts_combine",
     "qw_lora_workspace_bytes", "qw_lora_add",
+    "qw_route_scored_workspace_bytes", "qw_route_scored", "qw_rmsnorm", "qw_linear_workspace_bytes", "qgemm_linear",
 ]
 
 # test hooks (include/qw_tuning.h)
@@ -102,6 +107,13 @@ class qw_adapters(ctypes.Structure):
     ]
 
 
+class qw_epilogue(ctypes.Structure):
+    _fields_ = [
+        ("bias", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("bias_dtype", ctypes.c_int32),
+        ("residual_dtype", ctypes.c_int32), ("act", ctypes.c_int32), ("gated", ctypes.c_int32),
+    ]
+
+
 _lib = None
 
 
@@ -162,6 +174,12 @@ def lib():
         "qw_lora_workspace_bytes": (c_sz, [ctypes.POINTER(qw_adapters), c_i]),
         "qw_lora_add": (c_i, [ctypes.POINTER(qw_adapters), c_p, ctypes.POINTER(qw_groups), c_p, c_i, c_p, c_i,
                               c_p, c_sz, c_p]),
+        "qw_route_scored_workspace_bytes": (c_sz, [c_i, c_i, c_i, c_i]),
+        "qw_route_scored": (c_i, [c_p, c_i, c_i, c_i, c_i, c_i, c_p, c_i, c_i, c_i, c_i, ctypes.c_float, c_p, c_p, c_p,
+                                  c_p, c_p, c_sz, c_p]),
+        "qw_rmsnorm": (c_i, [c_p, c_i, c_p, c_i, c_p, c_i, ctypes.c_float, c_i, c_i, c_p, c_p, c_p, c_i, c_p, c_p]),
+        "qw_linear_workspace_bytes": (c_sz, [W, c_i]),
+        "qgemm_linear": (c_i, [W, c_p, c_i, c_p, c_i, ctypes.POINTER(qw_epilogue), c_p, c_i, c_p, c_sz, c_p]),
         "qw_tune_set": (c_i, [c_i, c_i]),
         "qw_tune_get": (c_i, [c_i]),
     }
@@ -825,6 +843,51 @@ def qw_route_topk(logits, top_k, normalize=True, workspace=None):
     return Routing(ids, weights, RowGroups(offsets, rows))
 
 
+@functools.lru_cache(maxsize=1024)
+def qw_route_scored_workspace_bytes(T, E, top_k, n_groups=1):
+    return int(lib().qw_route_scored_workspace_bytes(int(T), int(E), int(top_k), int(n_groups)))
+
+
+_SCORES = {"softmax": QW_ROUTE_SOFTMAX, "sigmoid": QW_ROUTE_SIGMOID}
+_GROUP_VALUES = {"max": QW_GROUP_MAX, "top2": QW_GROUP_TOP2}
+
+
+def qw_route_scored(logits, top_k, score="sigmoid", bias=None, n_groups=1, top_groups=None, group_by="top2", normalize=True,
+                    scale=1.0, workspace=None):
+    """The router of experts chosen by score + bias within the best
+    ``top_groups`` of ``n_groups`` groups (all of them by default) and weighted
+    by ``scale`` times their score, over the sum of the chosen ones' with
+    ``normalize``. score: "sigmoid" or "softmax" of logits (T, E; fp32, fp16 or
+    bf16); bias fp32 (E,); group_by: "top2" or "max". Returns a Routing."""
+    import torch
+    dt = _need_any(logits, "logits", 2)
+    T, E = logits.shape
+    top_k, n_groups = int(top_k), int(n_groups)
+    top_groups = n_groups if top_groups is None else int(top_groups)
+    if score not in _SCORES or group_by not in _GROUP_VALUES:
+        raise ValueError(f"score is one of {sorted(_SCORES)}, group_by one of {sorted(_GROUP_VALUES)}")
+    if n_groups < 1 or E % n_groups or not 1 <= top_groups <= n_groups:
+        raise ValueError("n_groups divides the number of experts, top_groups is in 1..n_groups")
+    if not 1 <= top_k <= E // n_groups * top_groups:
+        raise ValueError("top_k must be in 1..the number of experts in top_groups groups")
+    if bias is not None:
+        _need(bias, torch.float32, "bias", 1)
+        if bias.numel() != E:
+            raise ValueError(f"bias has {bias.numel()} entries, there are {E} experts")
+    dev = logits.device
+    ws = _workspace(workspace, qw_route_scored_workspace_bytes(T, E, top_k, n_groups), dev)
+    stream = _here(logits, ws) if bias is None else _here(logits, ws, bias)
+    ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
+    weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
+    offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
+    rows = torch.empty(T * top_k, dtype=torch.int32, device=dev)
+    _check(lib().qw_route_scored(logits.data_ptr(), dt, T, E, top_k, _SCORES[score], None if bias is None else bias.data_ptr(),
+                                 n_groups, top_groups, _GROUP_VALUES[group_by], 1 if normalize else 0, float(scale),
+                                 ids.data_ptr(), weights.data_ptr(), offsets.data_ptr(), rows.data_ptr(), ws.data_ptr(),
+                                 ws.numel(), stream), "qw_route_scored")
+    return Routing(ids, weights, RowGroups(offsets, rows))
+
+
 class ExpertWeights:
     """The packed weights of E experts of one shape, one behind another in
     each buffer (qw_experts). Buffers that are given are referenced, not
@@ -1022,3 +1085,133 @@ def qw_lora_add(adapters, x, groups, base, out_dtype=None, out=None, workspace=N
                              _w_dtype(base), Y.data_ptr(), _w_dtype(Y), ws.data_ptr(), ws.numel(), stream),
            "qw_lora_add")
     return Y
+
+
+# ---------------------------------------------- a layer around its projections
+
+@functools.lru_cache(maxsize=None)
+def _act_dtypes():
+    import torch
+    return {torch.float16: QW_DT_F16, torch.bfloat16: QW_DT_BF16, torch.float32: QW_DT_F32,
+            torch.float8_e4m3fn: QW_DT_E4M3, torch.int8: QW_DT_I8}
+
+
+class Normed:
+    """What qw_rmsnorm computes: ``y``, its ``scales`` (8-bit types, else None)
+    and ``residual``, the sum that was normalised (None without a residual)."""
+
+    def __init__(self, y, scales, residual):
+        self.y, self.scales, self.residual = y, scales, residual
+
+
+def qw_rmsnorm(x, weight, eps=1e-6, residual=None, residual_out=None, perm=None, out_dtype=None, out=None, scales=None):
+    """Root-mean-square norm of the rows of x + residual (M, K; each fp32, fp16
+    or bf16) times weight (K,). ``out_dtype`` may be torch.float8_e4m3fn or
+    torch.int8: then each row has a scale. ``perm`` (int32 (K,)): y in the INT4
+    format's channel order. The sum goes to ``residual_out`` (a new tensor by
+    default; residual_out=residual adds in place). Returns a Normed."""
+    import torch
+    x_dt, w_dt = _need_any(x, "x", 2), _need_any(weight, "weight", 1)
+    M, K = x.shape
+    if weight.numel() != K:
+        raise ValueError(f"weight has {weight.numel()} entries, x {K} columns")
+    dts = _act_dtypes()
+    y = out if out is not None else torch.empty((M, K), dtype=out_dtype or x.dtype, device=x.device)
+    if y.dtype not in dts or tuple(y.shape) != (M, K):
+        raise ValueError(f"output {tuple(y.shape)} {y.dtype}, expected {(M, K)} in fp16, bf16, fp32, e4m3 or int8")
+    y_dt = dts[y.dtype]
+    used = [x, weight, y]
+    r_dt = 0
+    if residual is None:
+        if residual_out is not None:
+            raise ValueError("residual_out without a residual")
+    else:
+        r_dt = _need_any(residual, "residual", 2)
+        if residual_out is None:
+            residual_out = torch.empty_like(residual)
+        if tuple(residual.shape) != (M, K) or tuple(residual_out.shape) != (M, K) or residual_out.dtype != residual.dtype:
+            raise ValueError(f"residual and residual_out must be {(M, K)} of one type")
+        used += [residual, residual_out]
+    if perm is not None:
+        _need(perm, torch.int32, "perm", 1)
+        if perm.numel() != K:
+            raise ValueError("perm must have K entries")
+        used.append(perm)
+    if y_dt in (QW_DT_E4M3, QW_DT_I8):
+        scales = scales if scales is not None else torch.empty(M, dtype=torch.float32, device=x.device)
+        _need(scales, torch.float32, "scales", 1)
+        if scales.numel() != M:
+            raise ValueError("scales must have one entry a row")
+        used.append(scales)
+    elif scales is not None:
+        raise ValueError("scales belong to the 8-bit types")
+    stream = _here(*used)
+    p = lambda t: None if t is None else t.data_ptr()
+    _check(lib().qw_rmsnorm(x.data_ptr(), x_dt, p(residual), r_dt, weight.data_ptr(), w_dt, float(eps), M, K, p(perm),
+                            p(residual_out), y.data_ptr(), y_dt, p(scales), stream), "qw_rmsnorm")
+    return Normed(y, scales, residual_out)
+
+
+_ACTS = {None: QW_ACT_NONE, "relu": QW_ACT_RELU, "silu": QW_ACT_SILU, "gelu": QW_ACT_GELU, "gelu_tanh": QW_ACT_GELU_TANH}
+
+
+def qw_linear_workspace_bytes(pw, M):
+    v = pw.view()
+    return int(lib().qw_linear_workspace_bytes(ctypes.byref(v), int(M)))
+
+
+def qgemm_linear(pw, X, bias=None, act=None, gated=False, residual=None, x_scales=None, out_dtype=None, out=None,
+                 workspace=None):
+    """Y = act(X . W^T + bias) + residual for any number of rows; gated (a merged
+    gate/up weight): act(gate) * up + residual. X (M, K) fp16 or bf16, or e4m3
+    or int8 with x_scales (M,), a scale a row; act: None, "relu", "silu", "gelu"
+    or "gelu_tanh". INT4: X in the weight's permuted channel order. out=residual
+    adds in place."""
+    import torch
+    dts = _act_dtypes()
+    if not isinstance(X, torch.Tensor) or not X.is_cuda or X.dtype not in dts or X.dtype == torch.float32:
+        raise TypeError("X must be a CUDA tensor of fp16, bf16, e4m3 or int8")
+    if X.dim() != 2 or X.shape[1] != pw.K:
+        raise ValueError(f"X has shape {tuple(X.shape)}, the weight's K is {pw.K}")
+    if act not in _ACTS:
+        raise ValueError(f"act is one of {list(_ACTS)}")
+    if gated and pw.N % 2:
+        raise ValueError("a merged gate/up weight has N = 2I rows")
+    M, N = X.shape[0], pw.N // 2 if gated else pw.N
+    x_dt = dts[X.dtype]
+    eight = x_dt in (QW_DT_E4M3, QW_DT_I8)
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype or (torch.bfloat16 if eight else X.dtype), device=X.device)
+    if tuple(out.shape) != (M, N):
+        raise ValueError(f"output shape {tuple(out.shape)}, expected {(M, N)}")
+    used = [X, out, pw.codes]
+    if eight != (x_scales is not None):
+        raise ValueError("x_scales belong to the 8-bit types, which need them")
+    if eight:
+        _need(x_scales, torch.float32, "x_scales", 1)
+        if x_scales.numel() != M:
+            raise ValueError("x_scales must have one entry a row")
+        used.append(x_scales)
+    ep = qw_epilogue(act=_ACTS[act], gated=1 if gated else 0)
+    if bias is not None:
+        ep.bias_dtype = _need_any(bias, "bias", 1)
+        if bias.numel() != pw.N:
+            raise ValueError(f"bias has {bias.numel()} entries, the weight {pw.N} rows")
+        ep.bias = bias.data_ptr()
+        used.append(bias)
+    if residual is not None:
+        ep.residual_dtype = _need_any(residual, "residual", 2)
+        if tuple(residual.shape) != (M, N):
+            raise ValueError(f"residual shape {tuple(residual.shape)}, expected {(M, N)}")
+        ep.residual = residual.data_ptr()
+        used.append(residual)
+    v = pw.view()
+    nb = int(lib().qw_linear_workspace_bytes(ctypes.byref(v), M))
+    ws = _workspace(workspace, nb, X.device) if nb else None
+    if ws is not None:
+        used.append(ws)
+    stream = _here(*used)
+    _check(lib().qgemm_linear(ctypes.byref(v), X.data_ptr(), x_dt, x_scales.data_ptr() if eight else None, M, ctypes.byref(ep),
+                              out.data_ptr(), _w_dtype(out), None if ws is None else ws.data_ptr(), nb, stream),
+           "qgemm_linear")
+    return out

@@ -89,7 +89,10 @@ typedef enum {
 } qw_status;
 
 typedef enum { QW_FMT_2BIT_G32 = 1, QW_FMT_NF4_B64 = 2, QW_FMT_INT4_G32 = 3 } qw_format;
-typedef enum { QW_DT_F16 = 1, QW_DT_BF16 = 2, QW_DT_F32 = 3 } qw_dtype;
+/* E4M3 (OCP fp8: 4 exponent bits, 3 mantissa bits, up to 448, no infinities)
+ * and I8 are activations with one fp32 scale a row (a value is the element
+ * times its row's scale); only the calls that say so take them. */
+typedef enum { QW_DT_F16 = 1, QW_DT_BF16 = 2, QW_DT_F32 = 3, QW_DT_E4M3 = 4, QW_DT_I8 = 5 } qw_dtype;
 
 /* Outlier channel score ("Profile-Guided Activation Outliers", section 4):
  * MEANABS = mean_n |W[n][c]| * mean_p |X[p][c]| (the |W| x |X| shorthand of
@@ -128,8 +131,8 @@ const char *qw_status_str(qw_status s);
 /* Kernel timing without launch gaps, for benchmarks and profilers. Arms the
  * next call of qw_select_outliers, qw_pack, qgemv_2bit, qgemv_nf4,
  * qgemv_2bit_grouped, qgemm_prefill, qw_group_rows, qw_route_topk,
- * qgemm_experts, qgemm_experts_combine or qw_lora_add made on the calling
- * host thread: the
+ * qw_route_scored, qgemm_experts, qgemm_experts_combine, qw_lora_add,
+ * qw_rmsnorm or qgemm_linear made on the calling host thread: the
  * first kernel that call dispatches records start_event when it begins
  * executing, and each of its kernels records stop_event when it ends, so
  * after the call the pair brackets exactly the device execution of its
@@ -584,6 +587,50 @@ qw_status qw_route_topk(const void *logits, qw_dtype dtype, int T, int E,
                         int32_t *offsets, int32_t *rows, void *workspace,
                         size_t workspace_bytes, void *stream);
 
+/* Scores of qw_route_scored, and how a group of experts is valued. */
+typedef enum { QW_ROUTE_SOFTMAX = 1, QW_ROUTE_SIGMOID = 2 } qw_route_score;
+typedef enum { QW_GROUP_MAX = 1, QW_GROUP_TOP2 = 2 } qw_group_value;
+/* Largest number of groups of experts of qw_route_scored. */
+#define QW_MAX_EXPERT_GROUPS 64
+
+/* Device workspace bytes of qw_route_scored (0 when none is needed or an
+ * argument is out of range). Host only. */
+size_t qw_route_scored_workspace_bytes(int T, int E, int top_k, int n_groups);
+
+/* The router of a layer whose experts are chosen by another value than their
+ * weight: with scores of each expert by itself, a bias that balances the
+ * experts' load and enters the choice alone, and groups of experts (one
+ * device's, say) of which only a few may be taken.
+ *   logits  device [T][E] of dtype F32, F16 or BF16. -inf marks an expert
+ *           the token may not take; NaN is taken as -inf.
+ *   bias    device fp32 [E], or NULL for zeros
+ *   score[e] = 1 / (1 + exp(-l[e])) (SIGMOID), or exp(l[e] - max l) / sum over
+ *           all E (SOFTMAX); choice[e] = score[e] + bias[e]. An expert whose
+ *           logit is -inf or whose choice is -inf or NaN is not taken (a
+ *           SOFTMAX row with a +inf logit takes none).
+ *   n_groups  the experts are cut into n_groups runs of E / n_groups (a
+ *           divisor of E, 1..QW_MAX_EXPERT_GROUPS). A group's value is its
+ *           largest choice (MAX) or the sum of its two largest (TOP2; of the
+ *           one there is where only one can be taken); the top_groups groups
+ *           of the largest values remain, equal ones by the lower group.
+ *           top_groups = n_groups: no group is left out.
+ *   ids     device int32 [T][top_k]: the experts of the largest choice in the
+ *           remaining groups, largest first, equal ones by the lower expert;
+ *           -1 where there are fewer than top_k.
+ *   weights device fp32 [T][top_k]: scale * score of the chosen expert
+ *           (without the bias), divided by the sum of the chosen ones' scores
+ *           when normalize != 0 (0 where that sum is 0); 0 where the id is -1.
+ *   offsets, rows, workspace: as qw_route_topk.
+ * Scores, choices and group values are computed and compared in 64 bits, so
+ * the order of experts is that of the formula but for differences of some
+ * 1e-15. Errors: INVALID_ARG (also top_k > E / n_groups * top_groups),
+ * ALIGNMENT, UNSUPPORTED (E > QW_MAX_GROUPS, T * top_k > QW_MAX_ROWS), HIP. */
+qw_status qw_route_scored(const void *logits, qw_dtype dtype, int T, int E, int top_k,
+                          qw_route_score score, const float *bias, int n_groups, int top_groups,
+                          qw_group_value group_by, int normalize, float scale, int32_t *ids,
+                          float *weights, int32_t *offsets, int32_t *rows, void *workspace,
+                          size_t workspace_bytes, void *stream);
+
 /* The packed weights of E experts of one shape. w is the view of expert 0;
  * its buffers hold the experts one behind another: codes [E][N][...],
  * scales [E][N][...], out_idx [E][n_out] and out_mask [E][K/32] (2-bit with
@@ -695,6 +742,98 @@ qw_status qw_lora_add(const qw_adapters *ad, const void *x, const qw_groups *g,
                       const void *base, qw_dtype base_dtype, void *out,
                       qw_dtype out_dtype, void *workspace, size_t workspace_bytes,
                       void *stream);
+
+/* ---- a layer around its projections --------------------------------------
+ *
+ * What stands before and behind a product: the norm that makes its
+ * activations, and bias, activation, gate and residual, which the product
+ * itself applies to its fp32 sums. (The OTF-LLM page names neither; its
+ * argument of section 1, that a token should read every weight once and pay
+ * for little else, is theirs too.) */
+
+/* Largest K of qw_rmsnorm. */
+#define QW_MAX_NORM_K 32768
+
+/* Root-mean-square norm of rows, with the residual's addition:
+ *   h[m][k] = x[m][k] + residual[m][k]   (x alone where residual is NULL)
+ *   y[m][j] = h[m][k] / sqrt(mean_k h[m][k]^2 + eps) * weight[k]
+ * with k = j, or k = perm[j]: y in the channel order of the INT4 format, as
+ * qw_permute_cols would leave it.
+ *   x            device [M][K] of x_dtype F16, BF16 or F32
+ *   residual     device [M][K] of residual_dtype (any of the three), or NULL
+ *   weight       device [K] of weight_dtype (any of the three)
+ *   perm         device int32 [K], or NULL; entries out of range give zeros
+ *   residual_out device [M][K] of residual_dtype: receives h (rounded once;
+ *                the norm takes the unrounded sum). NULL: h is not kept.
+ *   y            device [M][K] of y_dtype F16, BF16, F32, E4M3 or I8
+ *   y_scales     device fp32 [M] for E4M3 and I8 (else NULL): the row's
+ *                largest |y| over the type's largest number (448, 127), never
+ *                below 2^-100. An element is y over it, rounded to the
+ *                nearest (ties to even). A row with an infinity or a NaN gets
+ *                the scale NaN and zeros.
+ * A row is read whole before any of it is written: residual_out may be
+ * residual, and y may be x, if their types have one size and no other buffer
+ * overlaps. Sums are fp32 (a row of values beyond 2^60 overflows them), y is
+ * rounded once. eps is finite and >= 0 (a zero row at eps = 0 is NaN).
+ * Errors: INVALID_ARG (also residual_out without residual, y_scales given or
+ * missing against y_dtype), ALIGNMENT, UNSUPPORTED (K > QW_MAX_NORM_K,
+ * M > QW_MAX_ROWS), HIP. */
+qw_status qw_rmsnorm(const void *x, qw_dtype x_dtype, const void *residual,
+                     qw_dtype residual_dtype, const void *weight, qw_dtype weight_dtype,
+                     float eps, int M, int K, const int32_t *perm, void *residual_out, void *y,
+                     qw_dtype y_dtype, float *y_scales, void *stream);
+
+/* Activations of qgemm_linear: max(t, 0); t / (1 + exp(-t));
+ * t (1 + erf(t / sqrt 2)) / 2; t (1 + tanh(sqrt(2 / pi) (t + 0.044715 t^3))) / 2. */
+typedef enum {
+  QW_ACT_NONE = 0,
+  QW_ACT_RELU = 1,
+  QW_ACT_SILU = 2,
+  QW_ACT_GELU = 3,
+  QW_ACT_GELU_TANH = 4
+} qw_act;
+
+/* What qgemm_linear applies to its sums. A NULL pointer leaves its part out. */
+typedef struct {
+  const void *bias;       /* device [N] of bias_dtype F16, BF16 or F32 */
+  const void *residual;   /* device [M][N] (gated: [M][N/2]) of residual_dtype */
+  int32_t bias_dtype, residual_dtype;
+  int32_t act;            /* qw_act */
+  int32_t gated;          /* 0, or 1: w is a merged gate/up weight */
+} qw_epilogue;
+
+/* Device workspace bytes of qgemm_linear for M rows (0 when none is needed or
+ * an argument is out of range): fp32 partial sums where K is cut into parts.
+ * Host only. */
+size_t qw_linear_workspace_bytes(const qw_weight *w, int M);
+
+/* The product of any number of rows with one packed matrix, and what a layer
+ * does behind it, in one pass:
+ *   z[m][n] = x_scales[m] * sum_k X[m][k] w_hat[n][k] + bias[n]
+ *   Y[m][n] = act(z[m][n]) + residual[m][n]
+ * gated (N = 2I, gate rows 0..I-1 over up rows):
+ *   Y[m][n] = act(z[m][n]) * z[m][I + n] + residual[m][n],  n < I
+ * w_hat as in qgemv_2bit, qgemv_nf4 and qgemv_int4, anchors included (INT4: X
+ * in permuted channel order).
+ *   X        device [M][K] of x_dtype F16 or BF16 (x_scales NULL), or E4M3 or
+ *            I8 with x_scales device fp32 [M], as qw_rmsnorm writes them
+ *   ep       host struct, or NULL for none of it
+ *   Y        device [M][N or I] of y_dtype F16, BF16 or F32, rounded once.
+ *            ep->residual may be Y (added in place) where the types agree;
+ *            no other input may overlap Y.
+ *   workspace device scratch of workspace_bytes >=
+ *            qw_linear_workspace_bytes(w, M) (may be NULL when that is 0);
+ *            its contents on entry do not matter. Calls that overlap in time,
+ *            replays of captured ones among them, must not share it.
+ * Activations are finite (a row with an infinity or NaN gives values that are
+ * not, in that row alone) and below 2^110 in size. fp32 accumulation, and
+ * everything behind the sums in fp32.
+ * K must be a multiple of 64 and N K below 2^32. Errors: INVALID_ARG,
+ * ALIGNMENT, UNSUPPORTED (also M > QW_MAX_ROWS), HIP. */
+qw_status qgemm_linear(const qw_weight *w, const void *X, qw_dtype x_dtype,
+                       const float *x_scales, int M, const qw_epilogue *ep, void *Y,
+                       qw_dtype y_dtype, void *workspace, size_t workspace_bytes,
+                       void *stream);
 
 #ifdef __cplusplus
 }
