@@ -6,22 +6,29 @@
 
 namespace qw {
 
+// What stands behind the sums, and where it goes.
+struct Finish {
+  const float *x_scales;    // [M], null for 16-bit activations
+  const void *bias, *residual;
+  void *Y;                  // [M][out_n]
+  float *partial;           // [parts][M][N] where K is cut into parts
+  int bias_dtype, residual_dtype, y_dtype;
+  int act, gated;
+  int M, N, out_n;          // out_n: N, gated N / 2
+};
+
 struct LinearArgs {
   const void *X;            // [M][K]
-  const float *x_scales;    // [M], null for 16-bit activations
   const uint8_t *codes;
   const uint8_t *scales;
   const int32_t *idx;       // 2-bit anchors [n_out]
   const uint32_t *mask;     // 2-bit anchors [K/32]
   const uint16_t *wo;       // anchors [N][n_out_pad], fp16
-  void *Y;                  // [M][out_n]
-  float *partial;           // [parts][M][N] where K is cut into parts
-  const void *bias, *residual;
-  int bias_dtype, residual_dtype, act, gated;
-  int x_dtype, y_dtype;
-  int M, N, K, out_n;
+  int x_dtype;
+  int M, N, K;
   int n_out, n_out_pad;
   int row_tiles, col_tiles, parts;
+  Finish fin;
   float nf4[16];
 };
 
@@ -66,7 +73,7 @@ __device__ inline float activate(float z, int act) {
 
 // What stands behind the sums of four columns n.. of row m: s the sums, up the
 // sums of the up columns where gated. Stores the columns below out_n.
-__device__ inline void finish_four(const LinearArgs &a, int m, int n, f32x4 s, f32x4 up) {
+__device__ inline void finish_four(const Finish &a, int m, int n, f32x4 s, f32x4 up) {
   const int count = a.out_n - n;
   const bool vec = a.out_n % 4 == 0;
   if (a.x_scales) {
@@ -100,6 +107,18 @@ __device__ inline void finish_four(const LinearArgs &a, int m, int n, f32x4 s, f
     else
       reinterpret_cast<uint16_t *>(a.Y)[o + q] = (uint16_t)out_bits(s[q], a.y_dtype);
   }
+}
+
+// Four sums of a part of K: columns n.. of row m, those below `end`.
+__device__ inline void store_part(const Finish &a, int part, int m, int n, int end, f32x4 v) {
+  float *const o = a.partial + ((size_t)part * a.M + m) * a.N + n;
+  if (n + 4 <= end && a.out_n % 4 == 0) {  // then N is a multiple of 4, and n always
+    *reinterpret_cast<f32x4 *>(o) = v;
+    return;
+  }
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    if (n + q < end) o[q] = v[q];
 }
 
 // Activations as operands of type DT (the matrix cores' 16-bit types): eight
@@ -137,17 +156,49 @@ struct XLoad {
       return r;
     }
   }
-  // one element, as 16 bits of DT
-  static __device__ uint32_t one(const void *p, size_t element) {
-    if constexpr (XT == QW_DT_I8) {
-      return Op<QW_DT_F16>::bits((float)reinterpret_cast<const int8_t *>(p)[element]);
-    } else if constexpr (XT == QW_DT_E4M3) {
-      const uint32_t b = reinterpret_cast<const uint8_t *>(p)[element];
-      return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 1.0f, false)) & 0xFFFFu;
+};
+
+// Eight e4m3 or int8 numbers as bf16 (exact: no more than 8 significant bits).
+template <int XT>
+__device__ inline u32x4 eight_as_bf16(u32x2 r) {
+  u32x4 o;
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const uint32_t w = r[q];
+    if constexpr (XT == QW_DT_E4M3) {
+      o[2 * q] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, false));
+      o[2 * q + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, true));
     } else {
-      return reinterpret_cast<const uint16_t *>(p)[element];
+      // the upper halves of the numbers as fp32
+      const uint32_t f0 = __builtin_bit_cast(uint32_t, (float)(int8_t)w), f1 = __builtin_bit_cast(uint32_t, (float)(int8_t)(w >> 8));
+      const uint32_t f2 = __builtin_bit_cast(uint32_t, (float)(int8_t)(w >> 16)), f3 = __builtin_bit_cast(uint32_t, (float)(int8_t)(w >> 24));
+      o[2 * q] = __builtin_amdgcn_perm(f1, f0, 0x07060302u);
+      o[2 * q + 1] = __builtin_amdgcn_perm(f3, f2, 0x07060302u);
     }
   }
-};
+  return o;
+}
+// One element of activations, as 16 bits of DT.
+template <int XT, int DT>
+__device__ inline uint32_t one_as_16(const void *p, size_t element) {
+  if constexpr (XT == QW_DT_I8) {
+    return Op<DT>::bits((float)reinterpret_cast<const int8_t *>(p)[element]);
+  } else if constexpr (XT == QW_DT_E4M3) {
+    const uint32_t b = reinterpret_cast<const uint8_t *>(p)[element];
+    if constexpr (DT == QW_DT_BF16)
+      return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.0f, false)) & 0xFFFFu;
+    else
+      return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 1.0f, false)) & 0xFFFFu;
+  } else {
+    return reinterpret_cast<const uint16_t *>(p)[element];
+  }
+}
+
+// The narrow and the tall kernel of one format (linear_narrow_*.hip,
+// linear_tall_*.hip). row_blocks: 16-row blocks of a tile.
+template <int FMT>
+qw_status launch_linear_narrow(const LinearArgs &a, int row_blocks, hipStream_t s);
+template <int FMT>
+qw_status launch_linear_tall(const LinearArgs &a, int row_blocks, hipStream_t s);
 
 }  // namespace qw

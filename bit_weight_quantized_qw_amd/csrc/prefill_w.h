@@ -1,9 +1,11 @@
-// The prefill GEMM that keeps W out of LDS, for one matrix (prefill.hip) and
-// for rows grouped by expert (experts_tall.hip).
+// The prefill GEMM that keeps W out of LDS, for one matrix (prefill.hip), for
+// rows grouped by expert (experts_tall.hip) and for one matrix with what
+// follows the product (linear_tall.h).
 #pragma once
 
 #include <type_traits>
 
+#include "linear.h"
 #include "op16.h"
 #include "row_groups.h"
 
@@ -19,6 +21,9 @@ constexpr int NT = 256;
 
 struct PrefillArgs {
   static constexpr bool kGrouped = false;
+  static constexpr bool kLinear = false;
+  static constexpr bool kMask = false;  // 2-bit anchors: their channels of X enter as zeros
+  static constexpr bool kIn8 = false;   // X in 8 bits
   static constexpr int kRows = BM;  // rows of a tile
   static constexpr int kType = QW_DT_BF16;  // of X, of the weights as they enter, of 16-bit Y
   const uint16_t *X;       // [M][K] bf16
@@ -45,6 +50,24 @@ struct GroupedArgs : PrefillArgs {
   const int32_t *offsets, *rows;
   int G, n, x_div, by_slot;
   int n_tiles;             // column tiles of this launch
+};
+
+// The product of qgemm_linear: X in 8 or 16 bits, 2-bit anchors, K in parts, and
+// what stands behind the sums. M and X are those of a launch's rows.
+template <int ROWS, int XT, bool MASK>
+struct LinearTallArgs : PrefillArgs {
+  static constexpr bool kLinear = true;
+  static constexpr bool kMask = MASK;
+  static constexpr bool kIn8 = XT == QW_DT_E4M3 || XT == QW_DT_I8;
+  static constexpr int kRows = ROWS;
+  // e4m3 and int8 numbers are bf16 numbers
+  static constexpr int kType = XT == QW_DT_F16 ? QW_DT_F16 : QW_DT_BF16;
+  static __device__ u32x4 operand(u32x2 r) { return eight_as_bf16<XT>(r); }
+  static __device__ uint32_t one(const void *p, size_t i) { return one_as_16<XT, kType>(p, i); }
+  const uint32_t *mask;    // [K/32]
+  int m_first;             // the launch's first row among all
+  int n_tiles, parts;
+  Finish fin;
 };
 
 __device__ inline uint32_t f32_to_bf16_bits(float v) {
@@ -183,6 +206,7 @@ __global__ __launch_bounds__(256 * WM) void prefill_w_kernel(Args a) {
   const int wm = wv >> 2, wn = wv & 3;  // wave's row half (WM = 2) and column quarter
   int m_tile, n_tile;
   RowTile rt{0, 0, 0};
+  [[maybe_unused]] int part = 0, k_first = 0;  // the K part and its first element
   [[maybe_unused]] const uint32_t *codes = a.codes;  // of the tile's expert
   [[maybe_unused]] const void *scales = a.scales;
   if constexpr (Args::kGrouped) {
@@ -194,12 +218,21 @@ __global__ __launch_bounds__(256 * WM) void prefill_w_kernel(Args a) {
     const size_t weights = (size_t)rt.g * a.N * a.K;
     codes += FMT == QW_FMT_2BIT_G32 ? weights / 16 : weights / 8;
     scales = reinterpret_cast<const char *>(scales) + (FMT == QW_FMT_2BIT_G32 ? weights / 8 : weights / 16);
+  } else if constexpr (Args::kLinear) {
+    const int tiles = a.mt_count * a.n_tiles;
+    part = (int)blockIdx.x / tiles;
+    xcd_tile((int)blockIdx.x % tiles, a.mt_count, a.n_tiles, a.xcd_group, m_tile, n_tile);
   } else {
     xcd_tile((int)blockIdx.x, a.mt_count, (int)gridDim.x / a.mt_count, a.xcd_group, m_tile, n_tile);
   }
   const int m0 = m_tile * BM, n0 = a.n_begin + n_tile * (128 * NJ);
   const int K = a.K;
-  const int KT = K / BK;
+  int KT = K / BK;
+  if constexpr (Args::kLinear) {  // the part's steps
+    const int first = (int)((long long)KT * part / a.parts);
+    KT = (int)((long long)KT * (part + 1) / a.parts) - first;
+    k_first = first * BK;
+  }
   const int hk = lane >> 5;  // which 8 of each 16-wide k slice this lane holds
 
   if (kTab) {
@@ -214,9 +247,11 @@ __global__ __launch_bounds__(256 * WM) void prefill_w_kernel(Args a) {
   // ---- X prefetch registers (IM x 16 bytes per thread per step) ----
   // thread t copies 16-byte piece (t & 7) of rows (t >> 3) + 32 WM i, i < IM
   // (buffer loads: rows past M read through an out-of-range offset as 0)
-  u32x4 ra[IM];
+  typedef uint32_t xraw __attribute__((ext_vector_type(Args::kIn8 ? 2 : 4)));
+  constexpr uint32_t XB = Args::kIn8 ? 1 : 2;  // bytes of an element
+  xraw ra[IM];
   const int xr = tid >> 3, xc = (tid & 7) * 8;
-  const auto rx = pf_rsrc(a.X, (uint32_t)((size_t)a.M * K * 2));
+  const auto rx = pf_rsrc(reinterpret_cast<const char *>(a.X) + k_first * XB, (uint32_t)(((size_t)a.M * K - k_first) * XB));
   uint32_t xo[IM];
 #pragma unroll
   for (int i = 0; i < IM; ++i) {
@@ -226,21 +261,39 @@ __global__ __launch_bounds__(256 * WM) void prefill_w_kernel(Args a) {
       gm = q < rt.cnt ? (a.x_div ? x_row(a.rows[p], a.x_div, a.M) : p) : a.M;
       if (gm < 0) gm = a.M;
     }
-    xo[i] = gm < a.M ? (uint32_t)(((size_t)gm * K + xc) * 2) : kPfOob;
+    xo[i] = gm < a.M ? (uint32_t)(((size_t)gm * K + xc) * XB) : kPfOob;
   }
+  [[maybe_unused]] uint32_t drop = 0;  // anchor bits of this thread's eight channels
   // tiles at or past KT read as zeros (see the K loop below)
   auto load_x = [&](int kt) {
     const bool live = kt < KT;
-    const uint32_t k0b = live ? (uint32_t)kt * BK * 2 : 0u;
+    const uint32_t k0b = live ? (uint32_t)kt * BK * XB : 0u;
 #pragma unroll
-    for (int i = 0; i < IM; ++i)
-      ra[i] = __builtin_amdgcn_raw_buffer_load_b128(rx, (int)(live ? xo[i] : kPfOob), (int)k0b, 0);
+    for (int i = 0; i < IM; ++i) {
+      if constexpr (Args::kIn8)
+        ra[i] = __builtin_amdgcn_raw_buffer_load_b64(rx, (int)(live ? xo[i] : kPfOob), (int)k0b, 0);
+      else
+        ra[i] = __builtin_amdgcn_raw_buffer_load_b128(rx, (int)(live ? xo[i] : kPfOob), (int)k0b, 0);
+    }
+    if constexpr (Args::kMask)
+      drop = a.mask[(k_first + min(kt, KT - 1) * BK) / 32 + ((tid & 7) >> 2)] >> (8 * (tid & 3));
   };
   uint16_t *const xs = smem + xr * LDA + xc;  // + buf * BM * LDA + 32 WM i * LDA
   auto store_x = [&](int buf) {
 #pragma unroll
-    for (int i = 0; i < IM; ++i)
-      *reinterpret_cast<u32x4 *>(xs + buf * BM * LDA + 32 * WM * i * LDA) = ra[i];
+    for (int i = 0; i < IM; ++i) {
+      u32x4 v;
+      if constexpr (Args::kIn8)
+        v = Args::operand(ra[i]);
+      else
+        v = ra[i];
+      if constexpr (Args::kMask) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          v[q] &= ~(((drop >> (2 * q)) & 1 ? 0xFFFFu : 0u) | ((drop >> (2 * q + 1)) & 1 ? 0xFFFF0000u : 0u));
+      }
+      *reinterpret_cast<u32x4 *>(xs + buf * BM * LDA + 32 * WM * i * LDA) = v;
+    }
   };
 
   // ---- W registers of this lane's two columns, two sets (step parity) ----
@@ -252,11 +305,20 @@ __global__ __launch_bounds__(256 * WM) void prefill_w_kernel(Args a) {
   for (int j = 0; j < NJ; ++j) {
     gcol[j] = n0 + wn * 32 * NJ + j * 32 + (lane & 31);
     cvalid[j] = gcol[j] < a.N;
+    if constexpr (Args::kLinear) {
+      if (a.fin.gated) {  // 32 gate columns of a wave, and the same up columns
+        const int c = n_tile * 128 + wn * 32 + (lane & 31);
+        gcol[j] = c + j * a.fin.out_n;
+        cvalid[j] = c < a.fin.out_n;
+      }
+    }
   }
   const uint32_t cb = FMT == QW_FMT_2BIT_G32 ? (uint32_t)K / 4 : (uint32_t)K / 2;  // code bytes per column
   const uint32_t sb = FMT == QW_FMT_2BIT_G32 ? (uint32_t)K / 8 : (uint32_t)K / 16;  // scale bytes per column
-  const auto rcode = pf_rsrc(Args::kGrouped ? codes : a.codes, (uint32_t)((size_t)a.N * cb));
-  const auto rscale = pf_rsrc(Args::kGrouped ? scales : a.scales, (uint32_t)((size_t)a.N * sb));
+  constexpr int kCodeDiv = FMT == QW_FMT_2BIT_G32 ? 4 : 2, kScaleDiv = FMT == QW_FMT_2BIT_G32 ? 8 : 16;  // weights a byte
+  const uint32_t cskip = Args::kLinear ? (uint32_t)k_first / kCodeDiv : 0, sskip = Args::kLinear ? (uint32_t)k_first / kScaleDiv : 0;
+  const auto rcode = pf_rsrc(reinterpret_cast<const char *>(Args::kGrouped ? codes : a.codes) + cskip, (uint32_t)((size_t)a.N * cb - cskip));
+  const auto rscale = pf_rsrc(reinterpret_cast<const char *>(Args::kGrouped ? scales : a.scales) + sskip, (uint32_t)((size_t)a.N * sb - sskip));
   uint32_t co[NJ], so[NJ];
 #pragma unroll
   for (int j = 0; j < NJ; ++j) {
@@ -306,6 +368,18 @@ __global__ __launch_bounds__(256 * WM) void prefill_w_kernel(Args a) {
             top[j] = fmaxf(top[j], 8.0f * fmaxf(fabsf(f16_bits_to_f32((uint16_t)s)), fabsf(f16_bits_to_f32((uint16_t)(s >> 16)))));
           else
             top[j] = fmaxf(top[j], fabsf(__builtin_bit_cast(float, s)));
+        }
+      }
+    }
+    if constexpr (Args::kLinear) {  // and its anchors
+      for (int o = hk * 8; o < a.n_out; o += 16) {
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          u32x4 w = {0, 0, 0, 0};
+          if (cvalid[j]) w = *reinterpret_cast<const u32x4 *>(a.wo + (size_t)gcol[j] * a.n_out_pad + o);
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            top[j] = fmaxf(top[j], fmaxf(fabsf(f16_bits_to_f32((uint16_t)w[q])), fabsf(f16_bits_to_f32((uint16_t)(w[q] >> 16)))));
         }
       }
     }
@@ -494,6 +568,66 @@ __global__ __launch_bounds__(256 * WM) void prefill_w_kernel(Args a) {
     step(kt + 1, std::integral_constant<int, 1>{});
   }
 
+  // ---- anchors: 64 channels a step, their X gathered into a buffer, their
+  //      weights as the others enter ----
+  if constexpr (Args::kLinear) {
+    if (a.n_out > 0 && part == a.parts - 1) {
+      for (int o0 = 0; o0 < a.n_out; o0 += BK) {
+#pragma unroll 1
+        for (int i = 0; i < IM; ++i) {
+          const int gm = min(m0 + xr + 32 * WM * i, a.M - 1);  // rows past M are not stored
+          u32x4 v = {0, 0, 0, 0};
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            const int o = o0 + xc + q;
+            if (o < a.n_out) {
+              int k = o;
+              if (FMT == QW_FMT_2BIT_G32) {
+                k = a.idx[o];
+                if ((uint32_t)k >= (uint32_t)K) k = 0;
+              }
+              v[q >> 1] |= Args::one(a.X, (size_t)gm * K + k) << (16 * (q & 1));
+            }
+          }
+          *reinterpret_cast<u32x4 *>(xs + 32 * WM * i * LDA) = v;
+        }
+        __syncthreads();
+#pragma unroll 1
+        for (int kk = 0; kk < BK / 16; ++kk) {
+          const int o = o0 + kk * 16 + hk * 8;
+          bf16x8 fa[IM], fb[NJ];
+#pragma unroll
+          for (int i = 0; i < IM; ++i) fa[i] = *reinterpret_cast<const bf16x8 *>(ar + 32 * i * LDA + kk * 16);
+#pragma unroll
+          for (int j = 0; j < NJ; ++j) {
+            u32x4 w = {0, 0, 0, 0};
+            if (cvalid[j] && o < a.n_out_pad) w = *reinterpret_cast<const u32x4 *>(a.wo + (size_t)gcol[j] * a.n_out_pad + o);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              float lo = f16_bits_to_f32((uint16_t)w[q]), hi = f16_bits_to_f32((uint16_t)(w[q] >> 16));
+              if constexpr (kFit) {
+                lo *= fit[j];
+                hi *= fit[j];
+              }
+              w[q] = pack16x2<DT>(lo, hi);
+            }
+            fb[j] = __builtin_bit_cast(bf16x8, w);
+          }
+#pragma unroll
+          for (int i = 0; i < IM; ++i)
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) acc[i][j] = mma32<DT>(fa[i], fb[j], acc[i][j]);
+        }
+        __syncthreads();
+      }
+    }
+    // the accumulators are read by assembly below: the last products' results
+    // are there after 16 passes of 4 cycles
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_nop 15\n\ts_nop 15\n\ts_nop 15\n\ts_nop 15\n\ts_nop 15" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+  }
+
   // ---- epilogue: lane holds D[8*g + 4*(lane>>5) + r][lane & 31] of each
   //      32 x 32 block. Each wave passes its 32 x 64 slice of one row block
   //      at a time through its own LDS slab (the X buffers are free now):
@@ -541,6 +675,29 @@ __global__ __launch_bounds__(256 * WM) void prefill_w_kernel(Args a) {
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
     __builtin_amdgcn_wave_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+    if constexpr (Args::kLinear) {
+      // four columns a lane; gated: 32 columns of Y a row, the up sums beside them
+      const int per_row = a.fin.gated ? 8 : 8 * NJ, passes = per_row / 2;
+      const int lr = ln / per_row, lc = (ln % per_row) * 4;
+      const int n = a.fin.gated ? n_tile * 128 + wn * 32 + lc : n0 + wn * 32 * NJ + lc;
+      for (int pass = 0; pass < passes; ++pass) {
+        const int rr = pass * (64 / per_row) + lr, m = m0 + wm * (BM / WM) + i * 32 + rr;
+        auto sums = [&](int at) {
+          f32x4 v = *reinterpret_cast<const f32x4 *>(slab + rr * SL + at);
+          if constexpr (kFit) v *= *reinterpret_cast<const f32x4 *>(unfit + at);
+          return v;
+        };
+        if (m < a.M) {
+          if (a.parts > 1) {
+            store_part(a.fin, part, a.m_first + m, n, a.fin.out_n, sums(lc));
+            if (a.fin.gated && n < a.fin.out_n)
+              store_part(a.fin, part, a.m_first + m, n + a.fin.out_n, a.N, sums(32 * (NJ - 1) + lc));
+          } else if (n < a.fin.out_n) {
+            finish_four(a.fin, a.m_first + m, n, sums(lc), a.fin.gated ? sums(32 * (NJ - 1) + lc) : f32x4{0, 0, 0, 0});
+          }
+        }
+      }
+    } else
 #pragma unroll
     for (int pass = 0; pass < 32 / RP; ++pass) {
       const int rr = pass * RP + rr0;

@@ -49,7 +49,7 @@ EXPORTS = [
 # test hooks (include/qw_tuning.h)
 QW_TUNE_GEMV2_PATH, QW_TUNE_GEMV2_SPLIT, QW_TUNE_GEMV2_DEEP_RING = 1, 2, 3
 QW_TUNE_NF4_DEEP_RING, QW_TUNE_PREFILL_WIDE_TILES, QW_TUNE_INT4_PATH = 4, 5, 6
-QW_TUNE_EXPERTS_ROW_BLOCKS = 7
+QW_TUNE_EXPERTS_ROW_BLOCKS, QW_TUNE_LINEAR_ROW_BLOCKS, QW_TUNE_LINEAR_PARTS = 7, 8, 9
 QW_TUNE_AUTO = -1
 
 

@@ -44,7 +44,13 @@ typedef enum {
   /* Experts' products: -1 / 0 automatic, 1 the narrow kernel (16 rows), 2 or
    * 4 the wide one with tiles of that many 16-row blocks, 8 or 16 the tall
    * one where it takes the call (else 4). */
-  QW_TUNE_EXPERTS_ROW_BLOCKS = 7
+  QW_TUNE_EXPERTS_ROW_BLOCKS = 7,
+  /* qgemm_linear: -1 / 0 automatic, 1, 2 or 4 the narrow kernel with tiles of
+   * that many 16-row blocks, 8 or 16 the tall one. */
+  QW_TUNE_LINEAR_ROW_BLOCKS = 8,
+  /* qgemm_linear: -1 / 0 automatic, n >= 1 that many parts of K (at most one a
+   * step of 64, narrow tiles of 256). qw_linear_workspace_bytes follows it. */
+  QW_TUNE_LINEAR_PARTS = 9
 } qw_tune_key;
 
 #define QW_TUNE_AUTO (-1)

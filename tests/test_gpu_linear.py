@@ -13,9 +13,10 @@ pytestmark = pytest.mark.gpu
 ANCHORS = {"2bit": 0.035, "nf4": 0.0, "int4": 0.01}
 
 
-def case(fmt, M, K, N, kind, y, n_out=None, bias=None, act=None, gated=False, residual=None, seed=0, rounded=False, ws=None):
+def case(fmt, M, K, N, kind, y, n_out=None, bias=None, act=None, gated=False, residual=None, seed=0, rounded=None):
     import torch
     n_out = int(ANCHORS[fmt] * K) if n_out is None else n_out
+    rounded = M > 64 if rounded is None else rounded  # tall tiles from 65 rows on, if at all
     m = Matrix(fmt, N, K, n_out, seed)
     X, xs, x64 = activations(M, K, kind, seed + 1)
     g = torch.Generator().manual_seed(seed + 2)
@@ -23,7 +24,7 @@ def case(fmt, M, K, N, kind, y, n_out=None, bias=None, act=None, gated=False, re
     b = (0.5 * torch.randn(N, generator=g)).to(tdt(bias)) if bias else None
     r = torch.randn(M, width, generator=g).to(tdt(residual)) if residual else None
     got = qw.qgemm_linear(m.pw, X, bias=b.cuda() if bias else None, act=act, gated=gated, residual=r.cuda() if residual else None,
-                          x_scales=xs, out_dtype=tdt(y), workspace=ws)
+                          x_scales=xs, out_dtype=tdt(y))
     want, tol = linear64(m, x64, kind, rounded, b.double().numpy() if bias else None, act, gated,
                          r.double().numpy() if residual else None)
     assert got.dtype == tdt(y) and tuple(got.shape) == (M, width)
@@ -67,6 +68,65 @@ def test_lengths_of_the_sums(fmt, K):
 @pytest.mark.parametrize("M", [1, 2, 4, 15, 16, 17, 31, 32, 48, 64, 65, 100, 128, 129, 200])
 def test_rows(fmt, M):
     case(fmt, M, 512, 96, "f16", "f32", seed=M)
+
+
+# every kernel on the same shapes: 16-row blocks of a tile, parts of K
+PATHS = [(1, 1), (1, 3), (2, 1), (2, 4), (8, 1), (8, 3), (16, 1), (16, 2)]
+
+
+@pytest.mark.parametrize("blocks,parts", PATHS)
+@pytest.mark.parametrize("fmt,anchors", [("2bit", 0), ("2bit", 37), ("nf4", 0), ("int4", 0), ("int4", 70)])
+@pytest.mark.parametrize("kind", ["f16", "bf16", "e4m3", "i8"])
+def test_every_kernel(tune, blocks, parts, fmt, anchors, kind):
+    """K of five steps of 64 (an odd number, uneven parts), rows and columns past a tile's end."""
+    tune(qw.QW_TUNE_LINEAR_ROW_BLOCKS, blocks)
+    tune(qw.QW_TUNE_LINEAR_PARTS, parts)
+    case(fmt, 130, 832, 300, kind, "f32", anchors, seed=blocks + 20 * parts, rounded=blocks >= 8)
+
+
+@pytest.mark.parametrize("blocks,parts", PATHS)
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("N", [258, 516, 600])
+def test_every_kernel_and_epilogue(tune, blocks, parts, gated, N):
+    """Odd numbers of columns and of pairs, every epilogue part, each output type."""
+    tune(qw.QW_TUNE_LINEAR_ROW_BLOCKS, blocks)
+    tune(qw.QW_TUNE_LINEAR_PARTS, parts)
+    for y in ("f16", "bf16", "f32"):
+        case("int4", 100, 512, N, "bf16", y, 9, "f32", "silu", gated, "bf16", seed=N, rounded=blocks >= 8)
+    case("2bit", 270, 320, N + (0 if gated else 1), "i8", "f16", 11, "f16", "gelu", gated, "f16", seed=N + 1, rounded=blocks >= 8)
+
+
+def test_fp16_weights_of_any_size_keep_their_bits(tune):
+    """Tall tiles with fp16 activations: scales of 1e-6 and of 1e4, anchors larger
+    than the rest of their column."""
+    import torch
+    tune(qw.QW_TUNE_LINEAR_ROW_BLOCKS, 8)
+    X, _, x64 = activations(40, 256, "f16", 31)
+    for fmt, n_out in (("2bit", 9), ("int4", 9), ("nf4", 0)):
+        for size in (1e-6, 1.0, 1e4):
+            m = Matrix(fmt, 64, 256, n_out, 30)
+            if fmt == "nf4":
+                m.pw.scales.view(torch.float32).mul_(size)
+                m.W1, m.mag1 = m.W1 * np.float64(np.float32(size)), m.mag1 * size
+                extra = 2.0 ** -23  # the product with size, rounded
+            elif size < 1:
+                continue  # an fp16 Z would lose bits below 2^-14
+            else:  # fp16 scales: times a power of two, which is exact
+                size = 2.0 ** 10 if size > 1 else 1.0
+                m.pw.scales.view(torch.float16).mul_(size)
+                big = m.pw.out_w.view(torch.float16)
+                big.mul_(64.0)
+                idx = m.pw.out_idx.cpu().numpy()[:n_out] if fmt == "2bit" else np.arange(n_out)
+                keep = np.ones(256, bool)
+                keep[idx] = False
+                m.W1[:, keep] *= size
+                m.mag1[:, keep] *= size
+                m.W1[:, idx] *= 64
+                m.mag1[:, idx] *= 64
+                extra = 0.0
+            got = qw.qgemm_linear(m.pw, X, out_dtype=torch.float32)
+            want, tol = linear64(m, x64, "f16", True)
+            assert_close(got, want, tol + extra * (np.abs(x64) @ m.mag1.T), torch.float32, f"{fmt} {size}")
 
 
 def test_rows_do_not_depend_on_each_other_and_ends_stay():
