@@ -38,17 +38,20 @@ __device__ inline float load_any(const void *p, size_t i, int dt) {
   const uint32_t b = reinterpret_cast<const uint16_t *>(p)[i];
   return dt == QW_DT_F16 ? Op<QW_DT_F16>::value(b) : Op<QW_DT_BF16>::value(b);
 }
-// Four of them from i on; vec: i is a multiple of four elements.
+// Four 16-bit numbers.
+__device__ inline f32x4 four_of(u32x2 w, int dt) {
+  if (dt == QW_DT_F16)
+    return f32x4{Op<QW_DT_F16>::value(w[0] & 0xFFFFu), Op<QW_DT_F16>::value(w[0] >> 16), Op<QW_DT_F16>::value(w[1] & 0xFFFFu),
+                 Op<QW_DT_F16>::value(w[1] >> 16)};
+  return f32x4{Op<QW_DT_BF16>::value(w[0] & 0xFFFFu), Op<QW_DT_BF16>::value(w[0] >> 16), Op<QW_DT_BF16>::value(w[1] & 0xFFFFu),
+               Op<QW_DT_BF16>::value(w[1] >> 16)};
+}
+// Four of a vector from i on; vec: i is a multiple of four elements.
 __device__ inline f32x4 load_four(const void *p, size_t i, int dt, int count, bool vec) {
   f32x4 v = {0, 0, 0, 0};
   if (vec && count >= 4) {
     if (dt == QW_DT_F32) return *reinterpret_cast<const f32x4 *>(reinterpret_cast<const float *>(p) + i);
-    const u32x2 w = *reinterpret_cast<const u32x2 *>(reinterpret_cast<const uint16_t *>(p) + i);
-    if (dt == QW_DT_F16)
-      return f32x4{Op<QW_DT_F16>::value(w[0] & 0xFFFFu), Op<QW_DT_F16>::value(w[0] >> 16), Op<QW_DT_F16>::value(w[1] & 0xFFFFu),
-                   Op<QW_DT_F16>::value(w[1] >> 16)};
-    return f32x4{Op<QW_DT_BF16>::value(w[0] & 0xFFFFu), Op<QW_DT_BF16>::value(w[0] >> 16), Op<QW_DT_BF16>::value(w[1] & 0xFFFFu),
-                 Op<QW_DT_BF16>::value(w[1] >> 16)};
+    return four_of(*reinterpret_cast<const u32x2 *>(reinterpret_cast<const uint16_t *>(p) + i), dt);
   }
 #pragma unroll
   for (int q = 0; q < 4; ++q)
@@ -56,41 +59,50 @@ __device__ inline f32x4 load_four(const void *p, size_t i, int dt, int count, bo
   return v;
 }
 
-// The activation; act is uniform.
-__device__ inline float activate(float z, int act) {
+// The activation of four values; act is uniform.
+__device__ inline f32x4 activate(f32x4 z, int act) {
   switch (act) {
-    case QW_ACT_RELU: return z < 0.0f ? 0.0f : z;  // keeps a NaN
-    case QW_ACT_SILU: return z / (1.0f + expf(-z));
-    case QW_ACT_GELU: return 0.5f * z * erfcf(-0.70710678118654752f * z);
-    case QW_ACT_GELU_TANH: {
+    case QW_ACT_RELU:
+#pragma unroll
+      for (int q = 0; q < 4; ++q) z[q] = z[q] < 0.0f ? 0.0f : z[q];  // keeps a NaN
+      break;
+    case QW_ACT_SILU:
+#pragma unroll
+      for (int q = 0; q < 4; ++q) z[q] = z[q] / (1.0f + expf(-z[q]));
+      break;
+    case QW_ACT_GELU:
+#pragma unroll
+      for (int q = 0; q < 4; ++q) z[q] = 0.5f * z[q] * erfcf(-0.70710678118654752f * z[q]);
+      break;
+    case QW_ACT_GELU_TANH:
       // (1 + tanh u) / 2 = 1 / (1 + exp(-2 u)): no cancellation far below zero
-      const float u = 0.79788456080286536f * (z + 0.044715f * z * z * z);
-      return z / (1.0f + expf(-2.0f * u));
-    }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float u = 0.79788456080286536f * (z[q] + 0.044715f * z[q] * z[q] * z[q]);
+        z[q] = z[q] / (1.0f + expf(-2.0f * u));
+      }
+      break;
   }
   return z;
 }
 
-// What stands behind the sums of four columns n.. of row m: s the sums, up the
-// sums of the up columns where gated. Stores the columns below out_n.
-__device__ inline void finish_four(const Finish &a, int m, int n, f32x4 s, f32x4 up) {
-  const int count = a.out_n - n;
-  const bool vec = a.out_n % 4 == 0;
-  if (a.x_scales) {
-    const float f = a.x_scales[m];
-    s *= f;
-    if (a.gated) up *= f;
-  }
-  if (a.bias) {
-    s += load_four(a.bias, n, a.bias_dtype, count, true);
-    if (a.gated) up += load_four(a.bias, (size_t)a.out_n + n, a.bias_dtype, count, vec);
-  }
+// What stands behind four sums (up: those of the up columns where gated): the
+// row's scale, the columns' bias, the activation, the gate, the residual.
+__device__ inline f32x4 finish_values(const Finish &a, f32x4 s, f32x4 up, float scale, f32x4 bias, f32x4 bias_up, f32x4 residual) {
 #pragma unroll
-  for (int q = 0; q < 4; ++q) s[q] = activate(s[q], a.act);
-  if (a.gated) s *= up;
+  for (int q = 0; q < 4; ++q) s[q] = __builtin_fmaf(s[q], scale, bias[q]);
+  s = activate(s, a.act);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    if (a.gated) s[q] *= __builtin_fmaf(up[q], scale, bias_up[q]);
+    s[q] += residual[q];
+  }
+  return s;
+}
+// Stores four values at columns n.. of row m, those below out_n.
+__device__ inline void store_four(const Finish &a, int m, int n, f32x4 s) {
   const size_t o = (size_t)m * a.out_n + n;
-  if (a.residual) s += load_four(a.residual, o, a.residual_dtype, count, vec);
-  if (vec && count >= 4) {
+  if (a.out_n % 4 == 0 && n + 4 <= a.out_n) {
     if (a.y_dtype == QW_DT_F32)
       *reinterpret_cast<f32x4 *>(reinterpret_cast<float *>(a.Y) + o) = s;
     else
@@ -101,12 +113,24 @@ __device__ inline void finish_four(const Finish &a, int m, int n, f32x4 s, f32x4
   }
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
-    if (q >= count) continue;
+    if (n + q >= a.out_n) continue;
     if (a.y_dtype == QW_DT_F32)
       reinterpret_cast<float *>(a.Y)[o + q] = s[q];
     else
       reinterpret_cast<uint16_t *>(a.Y)[o + q] = (uint16_t)out_bits(s[q], a.y_dtype);
   }
+}
+
+// The inputs of four columns n.. of row m.
+__device__ inline float scale_at(const Finish &a, int m) { return a.x_scales ? a.x_scales[m] : 1.0f; }
+__device__ inline f32x4 bias_at(const Finish &a, int n) {
+  return a.bias ? load_four(a.bias, n, a.bias_dtype, a.out_n - n, true) : f32x4{0, 0, 0, 0};
+}
+__device__ inline f32x4 bias_up_at(const Finish &a, int n) {
+  return a.bias && a.gated ? load_four(a.bias, (size_t)a.out_n + n, a.bias_dtype, a.out_n - n, a.out_n % 4 == 0) : f32x4{0, 0, 0, 0};
+}
+__device__ inline f32x4 residual_at(const Finish &a, int m, int n) {
+  return a.residual ? load_four(a.residual, (size_t)m * a.out_n + n, a.residual_dtype, a.out_n - n, a.out_n % 4 == 0) : f32x4{0, 0, 0, 0};
 }
 
 // Four sums of a part of K: columns n.. of row m, those below `end`.
@@ -194,11 +218,14 @@ __device__ inline uint32_t one_as_16(const void *p, size_t element) {
   }
 }
 
-// The narrow and the tall kernel of one format (linear_narrow_*.hip,
-// linear_tall_*.hip). row_blocks: 16-row blocks of a tile.
+// The narrow kernel of one format (linear_narrow_*.hip); row_blocks: 16-row
+// blocks of a tile.
 template <int FMT>
 qw_status launch_linear_narrow(const LinearArgs &a, int row_blocks, hipStream_t s);
+// The tall kernel of one format (linear_tall_*.hip): the first high_tiles tiles
+// of columns by 256 rows, the others by 128.
+constexpr int tall_columns(bool gated) { return gated ? 128 : 256; }  // columns of Y of a tile
 template <int FMT>
-qw_status launch_linear_tall(const LinearArgs &a, int row_blocks, hipStream_t s);
+qw_status launch_linear_tall(const LinearArgs &a, int high_tiles, hipStream_t s);
 
 }  // namespace qw

@@ -23,25 +23,50 @@ __global__ __launch_bounds__(256) void join_kernel(Finish a, int parts, int col_
     s += load_four(a.partial, row + n, QW_DT_F32, a.out_n - n, vec);
     if (a.gated) up += load_four(a.partial, row + a.out_n + n, QW_DT_F32, a.out_n - n, vec);
   }
-  finish_four(a, m, n, s, up);
+  store_four(a, m, n, finish_values(a, s, up, scale_at(a, m), bias_at(a, n), bias_up_at(a, n), residual_at(a, m, n)));
 }
 
-// How a call runs: 16-row blocks of a tile (1 and 2 the narrow kernel, 8 and 16
-// the tall one) and parts of K.
+// How a call runs: the narrow kernel with tiles of row_blocks blocks of 16 rows,
+// or (row_blocks 0) the tall one, the first high_tiles tiles of columns with
+// 256 rows; and the parts of K.
 struct Plan {
-  int row_blocks, parts;
+  int row_blocks, high_tiles, parts;
 };
 
-Plan make_plan(int fmt, int M, int N, int K, bool gated) {
-  Plan p{1, 1};
-  const int forced = tune(QW_TUNE_LINEAR_ROW_BLOCKS);
-  p.row_blocks = forced > 0 ? forced : M <= 16 ? 1 : M <= 64 ? 2 : M <= 512 ? 8 : 16;
-  if (p.row_blocks >= 8) {
-    const long long tiles = (long long)((M + 16 * p.row_blocks - 1) / (16 * p.row_blocks)) * ((N + 255) / 256);
-    const long long full = p.row_blocks == 8 ? 512 : 256;
-    while (p.parts < 8 && tiles * p.parts * 2 <= full && K / 64 / (p.parts * 2) >= 8) p.parts *= 2;
+// Column tiles by 256 rows: whole rounds over the CUs, and the rest by tiles of
+// 128 rows, two workgroups a CU, in place of a round that fills few of them.
+// Times in rounds of high tiles; two low tiles side by side take 1.1 of one, a
+// low tile alone 0.6.
+int pick_high_tiles(int M, int nt) {
+  const int high = (M + 255) / 256, low = (M + 127) / 128;
+  double best = 1e30;
+  int best_n = 0;
+  for (int n = nt; n >= 0; --n) {
+    const long long h = (long long)high * n, l = (long long)low * (nt - n);
+    const double cost = (double)((h + 255) / 256) + (double)(l / 512) * 1.1 + (l % 512 == 0 ? 0.0 : l % 512 <= 256 ? 0.6 : 1.1);
+    if (cost < best - 1e-9) {
+      best = cost;
+      best_n = n;
+    }
   }
-  const int parts = tune(QW_TUNE_LINEAR_PARTS), step = p.row_blocks >= 8 ? 64 : 256;
+  return best_n;
+}
+
+Plan make_plan(int fmt, int M, int N, int K, bool gated) {
+  Plan p{0, 0, 1};
+  const int forced = tune(QW_TUNE_LINEAR_ROW_BLOCKS);
+  const int blocks = forced > 0 ? forced : M <= 16 ? 1 : M <= 64 ? 2 : 16;
+  if (blocks < 8) {
+    p.row_blocks = blocks;
+  } else {
+    const int cols = tall_columns(gated), nt = ((gated ? N / 2 : N) + cols - 1) / cols;
+    p.high_tiles = forced > 0 ? (forced >= 16 ? nt : 0) : pick_high_tiles(M, nt);
+    if (p.high_tiles == 0) {
+      const long long tiles = (long long)((M + 127) / 128) * nt;
+      while (p.parts < 8 && tiles * p.parts * 2 <= 512 && K / 64 / (p.parts * 2) >= 8) p.parts *= 2;
+    }
+  }
+  const int parts = tune(QW_TUNE_LINEAR_PARTS), step = p.row_blocks ? 256 : 64;
   if (parts > 0) p.parts = parts < K / step ? parts : K / step > 1 ? K / step : 1;
   return p;
 }
@@ -54,7 +79,7 @@ bool takes(const qw_weight *w, int M) {
 
 template <int FMT>
 qw_status run(const LinearArgs &a, const Plan &p, hipStream_t s) {
-  if (p.row_blocks >= 8) return launch_linear_tall<FMT>(a, p.row_blocks, s);
+  if (p.row_blocks == 0) return launch_linear_tall<FMT>(a, p.high_tiles, s);
   return launch_linear_narrow<FMT>(a, p.row_blocks, s);
 }
 
@@ -65,8 +90,12 @@ extern "C" {
 
 size_t qw_linear_workspace_bytes(const qw_weight *w, int M) {
   if (!qw::takes(w, M)) return 0;
-  const qw::Plan p = qw::make_plan(w->format, M, w->N, w->K, false);
-  return p.parts > 1 ? (size_t)p.parts * (size_t)M * (size_t)w->N * sizeof(float) : 0;
+  int parts = 1;  // gated or not
+  for (int gated = 0; gated < 2; ++gated) {
+    const qw::Plan p = qw::make_plan(w->format, M, w->N, w->K, gated != 0);
+    if (p.parts > parts) parts = p.parts;
+  }
+  return parts > 1 ? (size_t)parts * (size_t)M * (size_t)w->N * sizeof(float) : 0;
 }
 
 qw_status qgemm_linear(const qw_weight *w, const void *X, qw_dtype x_dtype, const float *x_scales, int M,

@@ -8,9 +8,11 @@
 namespace qw {
 namespace {
 
-template <int FMT, int ROWS, int XT, bool MASK>
-qw_status launch_tall(const LinearArgs &l, hipStream_t s) {
-  using Args = LinearTallArgs<ROWS, XT, MASK>;
+// Columns n_begin .. n_begin + columns of Y, by tiles of ROWS rows.
+template <int FMT, int ROWS, int XT, bool MASK, bool GATED>
+qw_status launch_columns(const LinearArgs &l, int n_begin, int columns, hipStream_t s) {
+  if (columns <= 0) return QW_OK;
+  using Args = LinearTallArgs<ROWS, XT, MASK, GATED>;
   constexpr auto kernel = prefill_w_kernel<FMT, true, 2, 1, Args>;
   const size_t lds = prefill_w_lds(ROWS, 2);
   QW_HIP_TRY(hipFuncSetAttribute(reinterpret_cast<const void *>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds));
@@ -26,8 +28,8 @@ qw_status launch_tall(const LinearArgs &l, hipStream_t s) {
   a.n_out_pad = l.n_out_pad;
   a.xcd_group = 4;
   for (int i = 0; i < 16; ++i) a.nf4[i] = l.nf4[i];
-  const int cols = l.fin.gated ? 128 : 256;
-  a.n_tiles = (l.fin.out_n + cols - 1) / cols;
+  a.n_begin = n_begin;
+  a.n_tiles = (columns + tall_columns(GATED) - 1) / tall_columns(GATED);
   a.parts = l.parts;
   a.fin = l.fin;
   // offsets into X have 32 bits: as many rows a launch as lie below them
@@ -46,23 +48,35 @@ qw_status launch_tall(const LinearArgs &l, hipStream_t s) {
   return QW_OK;
 }
 
+template <int FMT, int XT, bool MASK, bool GATED>
+qw_status launch_tiles(const LinearArgs &a, int high_tiles, hipStream_t s) {
+  const int most = (a.fin.out_n + tall_columns(GATED) - 1) / tall_columns(GATED) * tall_columns(GATED);
+  const int high = high_tiles * tall_columns(GATED) < most ? high_tiles * tall_columns(GATED) : most;
+  QW_TRY((launch_columns<FMT, 256, XT, MASK, GATED>(a, 0, high < a.fin.out_n ? high : a.fin.out_n, s)));
+  return launch_columns<FMT, 128, XT, MASK, GATED>(a, high, a.fin.out_n - high, s);
+}
+
+template <int FMT, int XT, bool MASK>
+qw_status launch_gated(const LinearArgs &a, int high_tiles, hipStream_t s) {
+  return a.fin.gated ? launch_tiles<FMT, XT, MASK, true>(a, high_tiles, s) : launch_tiles<FMT, XT, MASK, false>(a, high_tiles, s);
+}
+
 template <int FMT, int XT>
-qw_status launch_tall_type(const LinearArgs &a, int row_blocks, hipStream_t s) {
+qw_status launch_tall_type(const LinearArgs &a, int high_tiles, hipStream_t s) {
   if constexpr (FMT == QW_FMT_2BIT_G32)
-    if (a.n_out > 0)
-      return row_blocks <= 8 ? launch_tall<FMT, 128, XT, true>(a, s) : launch_tall<FMT, 256, XT, true>(a, s);
-  return row_blocks <= 8 ? launch_tall<FMT, 128, XT, false>(a, s) : launch_tall<FMT, 256, XT, false>(a, s);
+    if (a.n_out > 0) return launch_gated<FMT, XT, true>(a, high_tiles, s);
+  return launch_gated<FMT, XT, false>(a, high_tiles, s);
 }
 
 }  // namespace
 
 template <int FMT>
-qw_status launch_linear_tall(const LinearArgs &a, int row_blocks, hipStream_t s) {
+qw_status launch_linear_tall(const LinearArgs &a, int high_tiles, hipStream_t s) {
   switch (a.x_dtype) {
-    case QW_DT_F16: return launch_tall_type<FMT, QW_DT_F16>(a, row_blocks, s);
-    case QW_DT_BF16: return launch_tall_type<FMT, QW_DT_BF16>(a, row_blocks, s);
-    case QW_DT_E4M3: return launch_tall_type<FMT, QW_DT_E4M3>(a, row_blocks, s);
-    default: return launch_tall_type<FMT, QW_DT_I8>(a, row_blocks, s);
+    case QW_DT_F16: return launch_tall_type<FMT, QW_DT_F16>(a, high_tiles, s);
+    case QW_DT_BF16: return launch_tall_type<FMT, QW_DT_BF16>(a, high_tiles, s);
+    case QW_DT_E4M3: return launch_tall_type<FMT, QW_DT_E4M3>(a, high_tiles, s);
+    default: return launch_tall_type<FMT, QW_DT_I8>(a, high_tiles, s);
   }
 }
 

@@ -22,6 +22,7 @@ constexpr int NT = 256;
 struct PrefillArgs {
   static constexpr bool kGrouped = false;
   static constexpr bool kLinear = false;
+  static constexpr bool kGated = false;  // qgemm_linear: act(gate) * up
   static constexpr bool kMask = false;  // 2-bit anchors: their channels of X enter as zeros
   static constexpr bool kIn8 = false;   // X in 8 bits
   static constexpr int kRows = BM;  // rows of a tile
@@ -54,9 +55,10 @@ struct GroupedArgs : PrefillArgs {
 
 // The product of qgemm_linear: X in 8 or 16 bits, 2-bit anchors, K in parts, and
 // what stands behind the sums. M and X are those of a launch's rows.
-template <int ROWS, int XT, bool MASK>
+template <int ROWS, int XT, bool MASK, bool GATED>
 struct LinearTallArgs : PrefillArgs {
   static constexpr bool kLinear = true;
+  static constexpr bool kGated = GATED;
   static constexpr bool kMask = MASK;
   static constexpr bool kIn8 = XT == QW_DT_E4M3 || XT == QW_DT_I8;
   static constexpr int kRows = ROWS;
@@ -305,12 +307,10 @@ __global__ __launch_bounds__(256 * WM) void prefill_w_kernel(Args a) {
   for (int j = 0; j < NJ; ++j) {
     gcol[j] = n0 + wn * 32 * NJ + j * 32 + (lane & 31);
     cvalid[j] = gcol[j] < a.N;
-    if constexpr (Args::kLinear) {
-      if (a.fin.gated) {  // 32 gate columns of a wave, and the same up columns
-        const int c = n_tile * 128 + wn * 32 + (lane & 31);
-        gcol[j] = c + j * a.fin.out_n;
-        cvalid[j] = c < a.fin.out_n;
-      }
+    if constexpr (Args::kGated) {  // 32 gate columns of a wave, and the same up columns
+      const int c = a.n_begin + n_tile * 128 + wn * 32 + (lane & 31);
+      gcol[j] = c + j * a.fin.out_n;
+      cvalid[j] = c < a.fin.out_n;
     }
   }
   const uint32_t cb = FMT == QW_FMT_2BIT_G32 ? (uint32_t)K / 4 : (uint32_t)K / 2;  // code bytes per column
@@ -657,6 +657,112 @@ __global__ __launch_bounds__(256 * WM) void prefill_w_kernel(Args a) {
                           (uint32_t)((4 * (ln >> 5) * SL + (ln & 31)) * 4);
   const int gc = n0 + wn * 32 * NJ + cc;
   static_assert(4 * WM * 32 * SL * 4 <= prefill_w_lds(BM, NJ), "slabs fit in the X buffers");
+  if constexpr (Args::kLinear) {
+    // qgemm_linear: H row blocks go through a wave's slab at a time, so that the
+    // code of what stands behind the sums is there IM / H times. Four columns a
+    // lane (gated: 32 of a wave, the up sums beside them), pass t of the wave's
+    // rows being the rows from t kRowsAPass on. What is added comes from memory
+    // kAhead passes ahead: asked for where it is used, every pass would wait.
+    constexpr int H = IM >= 8 ? 2 : 1;
+    static_assert(4 * WM * H * 32 * SL * 4 <= prefill_w_lds(BM, NJ), "slabs fit in the X buffers");
+    float *const high = reinterpret_cast<float *>(smem) + wv * H * 32 * SL;
+    const uint32_t high_w = (uint32_t)reinterpret_cast<uintptr_t>(high) + (uint32_t)((4 * (ln >> 5) * SL + (ln & 31)) * 4);
+    constexpr int kPerRow = Args::kGated ? 8 : 8 * NJ, kRowsAPass = 64 / kPerRow, kPasses = H * 32 / kRowsAPass;
+    constexpr int kAhead = 4;
+    static_assert(kPasses % kAhead == 0, "passes go by kAhead");
+    const int lr = ln / kPerRow, lc = (ln % kPerRow) * 4;
+    const int n_lane = Args::kGated ? a.n_begin + n_tile * 128 + wn * 32 + lc : n0 + wn * 32 * NJ + lc;
+    const int row0 = m0 + wm * (BM / WM) + lr;
+    const bool inside = n_lane < a.fin.out_n;
+    f32x4 bias = {0, 0, 0, 0}, bias_up = {0, 0, 0, 0};
+    u32x4 res[kAhead];
+    float scale[kAhead];
+    auto sums_at = [&](int rr, int at) {
+      f32x4 v = *reinterpret_cast<const f32x4 *>(high + rr * SL + at);
+      if constexpr (kFit) v *= *reinterpret_cast<const f32x4 *>(unfit + at);
+      return v;
+    };
+    // the residual as it lies in memory where four columns are one load
+    const bool raw = a.fin.residual && a.fin.out_n % 4 == 0;
+    auto ask = [&](int t, u32x4 &r, float &f) {
+      const int m = a.m_first + min(row0 + t * kRowsAPass, a.M - 1);
+      f = scale_at(a.fin, m);
+      r = u32x4{0, 0, 0, 0};
+      if (!a.fin.residual || !inside) return;
+      if (!raw) {
+        r = __builtin_bit_cast(u32x4, residual_at(a.fin, m, n_lane));
+        return;
+      }
+      const size_t o = (size_t)m * a.fin.out_n + n_lane;
+      if (a.fin.residual_dtype == QW_DT_F32) {
+        r = *reinterpret_cast<const u32x4 *>(reinterpret_cast<const float *>(a.fin.residual) + o);
+      } else {
+        const u32x2 w = *reinterpret_cast<const u32x2 *>(reinterpret_cast<const uint16_t *>(a.fin.residual) + o);
+        r[0] = w[0];
+        r[1] = w[1];
+      }
+    };
+    auto residual_of = [&](u32x4 w) {
+      if (!raw || a.fin.residual_dtype == QW_DT_F32) return __builtin_bit_cast(f32x4, w);
+      return four_of(u32x2{w[0], w[1]}, a.fin.residual_dtype);
+    };
+    if (a.parts == 1) {
+      if (inside) {
+        bias = bias_at(a.fin, n_lane);
+        bias_up = bias_up_at(a.fin, n_lane);
+      }
+#pragma unroll
+      for (int t = 0; t < kAhead; ++t) ask(t, res[t], scale[t]);
+    }
+#pragma unroll
+    for (int i0 = 0; i0 < IM; i0 += H) {
+#pragma unroll
+      for (int i = 0; i < H; ++i)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+          for (int g = 0; g < 4; ++g)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              asm volatile("ds_write_b32 %0, %1 offset:%2"
+                           :
+                           : "v"(high_w), "a"(acc[i0 + i][j][4 * g + r]), "i"(((i * 32 + 8 * g + r) * SL + j * 32) * 4)
+                           : "memory");
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+      __builtin_amdgcn_wave_barrier();
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+      const int t0 = i0 / H * kPasses;
+      if (a.parts > 1) {
+#pragma unroll 1
+        for (int t = 0; t < kPasses; ++t) {
+          const int rr = t * kRowsAPass + lr, m = row0 + (t0 + t) * kRowsAPass;
+          if (m >= a.M || !inside) continue;
+          store_part(a.fin, part, a.m_first + m, n_lane, a.fin.out_n, sums_at(rr, lc));
+          if constexpr (Args::kGated) store_part(a.fin, part, a.m_first + m, n_lane + a.fin.out_n, a.N, sums_at(rr, 32 + lc));
+        }
+      } else {
+#pragma unroll 1
+        for (int t1 = 0; t1 < kPasses; t1 += kAhead) {
+#pragma unroll
+          for (int t = 0; t < kAhead; ++t) {
+            const int rr = (t1 + t) * kRowsAPass + lr, m = row0 + (t0 + t1 + t) * kRowsAPass;
+            const f32x4 r = residual_of(res[t]);
+            const float f = scale[t];
+            ask(t0 + t1 + t + kAhead, res[t], scale[t]);  // past the last row: that row's
+            f32x4 up = {0, 0, 0, 0};
+            if constexpr (Args::kGated) up = sums_at(rr, 32 + lc);
+            const f32x4 v = finish_values(a.fin, sums_at(rr, lc), up, f, bias, bias_up, r);
+            if (m < a.M && inside) store_four(a.fin, a.m_first + m, n_lane, v);
+          }
+        }
+      }
+      // the slab is rewritten by the next row blocks
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+      __builtin_amdgcn_wave_barrier();
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+    }
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < IM; ++i) {
     // ds_write with the accumulator register as data operand: a plain store
@@ -675,29 +781,6 @@ __global__ __launch_bounds__(256 * WM) void prefill_w_kernel(Args a) {
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
     __builtin_amdgcn_wave_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
-    if constexpr (Args::kLinear) {
-      // four columns a lane; gated: 32 columns of Y a row, the up sums beside them
-      const int per_row = a.fin.gated ? 8 : 8 * NJ, passes = per_row / 2;
-      const int lr = ln / per_row, lc = (ln % per_row) * 4;
-      const int n = a.fin.gated ? n_tile * 128 + wn * 32 + lc : n0 + wn * 32 * NJ + lc;
-      for (int pass = 0; pass < passes; ++pass) {
-        const int rr = pass * (64 / per_row) + lr, m = m0 + wm * (BM / WM) + i * 32 + rr;
-        auto sums = [&](int at) {
-          f32x4 v = *reinterpret_cast<const f32x4 *>(slab + rr * SL + at);
-          if constexpr (kFit) v *= *reinterpret_cast<const f32x4 *>(unfit + at);
-          return v;
-        };
-        if (m < a.M) {
-          if (a.parts > 1) {
-            store_part(a.fin, part, a.m_first + m, n, a.fin.out_n, sums(lc));
-            if (a.fin.gated && n < a.fin.out_n)
-              store_part(a.fin, part, a.m_first + m, n + a.fin.out_n, a.N, sums(32 * (NJ - 1) + lc));
-          } else if (n < a.fin.out_n) {
-            finish_four(a.fin, a.m_first + m, n, sums(lc), a.fin.gated ? sums(32 * (NJ - 1) + lc) : f32x4{0, 0, 0, 0});
-          }
-        }
-      }
-    } else
 #pragma unroll
     for (int pass = 0; pass < 32 / RP; ++pass) {
       const int rr = pass * RP + rr0;
