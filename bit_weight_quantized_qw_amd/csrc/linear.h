@@ -86,16 +86,15 @@ __device__ inline f32x4 activate(f32x4 z, int act) {
   return z;
 }
 
-// What stands behind four sums (up: those of the up columns where gated): the
-// row's scale, the columns' bias, the activation, the gate, the residual.
-__device__ inline f32x4 finish_values(const Finish &a, f32x4 s, f32x4 up, float scale, f32x4 bias, f32x4 bias_up, f32x4 residual) {
+// What stands behind four sums (up: those of the up columns where gated) but the
+// residual: the row's scale, the columns' bias, the activation, the gate.
+__device__ inline f32x4 shape_values(const Finish &a, f32x4 s, f32x4 up, float scale, f32x4 bias, f32x4 bias_up) {
 #pragma unroll
   for (int q = 0; q < 4; ++q) s[q] = __builtin_fmaf(s[q], scale, bias[q]);
   s = activate(s, a.act);
+  if (a.gated) {
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    if (a.gated) s[q] *= __builtin_fmaf(up[q], scale, bias_up[q]);
-    s[q] += residual[q];
+    for (int q = 0; q < 4; ++q) s[q] *= __builtin_fmaf(up[q], scale, bias_up[q]);
   }
   return s;
 }

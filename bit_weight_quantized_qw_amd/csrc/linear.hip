@@ -23,7 +23,7 @@ __global__ __launch_bounds__(256) void join_kernel(Finish a, int parts, int col_
     s += load_four(a.partial, row + n, QW_DT_F32, a.out_n - n, vec);
     if (a.gated) up += load_four(a.partial, row + a.out_n + n, QW_DT_F32, a.out_n - n, vec);
   }
-  store_four(a, m, n, finish_values(a, s, up, scale_at(a, m), bias_at(a, n), bias_up_at(a, n), residual_at(a, m, n)));
+  store_four(a, m, n, shape_values(a, s, up, scale_at(a, m), bias_at(a, n), bias_up_at(a, n)) + residual_at(a, m, n));
 }
 
 // How a call runs: the narrow kernel with tiles of row_blocks blocks of 16 rows,

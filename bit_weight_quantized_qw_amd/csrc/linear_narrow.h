@@ -287,8 +287,8 @@ __global__ __launch_bounds__(kThreads, 2) void narrow_kernel(LinearArgs a) {
       store_part(a.fin, part_of, m, c0 + c, a.fin.out_n, total(c));
       if (a.fin.gated) store_part(a.fin, part_of, m, a.fin.out_n + c0 + c, a.N, up);
     } else {
-      store_four(a.fin, m, c0 + c, finish_values(a.fin, total(c), up, scale_at(a.fin, m), bias_at(a.fin, c0 + c),
-                                                 bias_up_at(a.fin, c0 + c), residual_at(a.fin, m, c0 + c)));
+      const f32x4 v = shape_values(a.fin, total(c), up, scale_at(a.fin, m), bias_at(a.fin, c0 + c), bias_up_at(a.fin, c0 + c));
+      store_four(a.fin, m, c0 + c, v + residual_at(a.fin, m, c0 + c));
     }
   }
 }

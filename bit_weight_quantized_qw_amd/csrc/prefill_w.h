@@ -658,25 +658,27 @@ __global__ __launch_bounds__(256 * WM) void prefill_w_kernel(Args a) {
   const int gc = n0 + wn * 32 * NJ + cc;
   static_assert(4 * WM * 32 * SL * 4 <= prefill_w_lds(BM, NJ), "slabs fit in the X buffers");
   if constexpr (Args::kLinear) {
-    // qgemm_linear: H row blocks go through a wave's slab at a time, so that the
-    // code of what stands behind the sums is there IM / H times. Four columns a
-    // lane (gated: 32 of a wave, the up sums beside them), pass t of the wave's
-    // rows being the rows from t kRowsAPass on. What is added comes from memory
-    // kAhead passes ahead: asked for where it is used, every pass would wait.
+    // qgemm_linear: H row blocks go through a wave's slab at a time, in two
+    // steps: activation and gate in the slab (a loop, its code is long), then the
+    // residual's addition and the stores (unrolled). Four columns a lane (gated:
+    // 32 of a wave, the up sums beside them), pass t of the wave's rows being the
+    // rows from t kRowsAPass on. The residual of a whole slab is on its way
+    // before its sums are: with one workgroup on a CU nothing else hides its
+    // latency (2048 x 28672 with a residual in 16 bits: four passes ahead 130 us
+    // more than without one).
     constexpr int H = IM >= 8 ? 2 : 1;
     static_assert(4 * WM * H * 32 * SL * 4 <= prefill_w_lds(BM, NJ), "slabs fit in the X buffers");
     float *const high = reinterpret_cast<float *>(smem) + wv * H * 32 * SL;
     const uint32_t high_w = (uint32_t)reinterpret_cast<uintptr_t>(high) + (uint32_t)((4 * (ln >> 5) * SL + (ln & 31)) * 4);
     constexpr int kPerRow = Args::kGated ? 8 : 8 * NJ, kRowsAPass = 64 / kPerRow, kPasses = H * 32 / kRowsAPass;
-    constexpr int kAhead = 4;
-    static_assert(kPasses % kAhead == 0, "passes go by kAhead");
     const int lr = ln / kPerRow, lc = (ln % kPerRow) * 4;
     const int n_lane = Args::kGated ? a.n_begin + n_tile * 128 + wn * 32 + lc : n0 + wn * 32 * NJ + lc;
     const int row0 = m0 + wm * (BM / WM) + lr;
     const bool inside = n_lane < a.fin.out_n;
     f32x4 bias = {0, 0, 0, 0}, bias_up = {0, 0, 0, 0};
-    u32x4 res[kAhead];
-    float scale[kAhead];
+    u32x4 res[kPasses];
+    float scale[kPasses];
+    const bool shaped = Args::kGated || a.fin.act != QW_ACT_NONE;  // the first step is needed
     auto sums_at = [&](int rr, int at) {
       f32x4 v = *reinterpret_cast<const f32x4 *>(high + rr * SL + at);
       if constexpr (kFit) v *= *reinterpret_cast<const f32x4 *>(unfit + at);
@@ -712,10 +714,12 @@ __global__ __launch_bounds__(256 * WM) void prefill_w_kernel(Args a) {
         bias_up = bias_up_at(a.fin, n_lane);
       }
 #pragma unroll
-      for (int t = 0; t < kAhead; ++t) ask(t, res[t], scale[t]);
+      for (int t = 0; t < kPasses; ++t) ask(t, res[t], scale[t]);
     }
-#pragma unroll
-    for (int i0 = 0; i0 < IM; i0 += H) {
+    // (a call for each slab, inlined: too long for the compiler to unroll a loop
+    // of them, and a loop would move the accumulators to memory)
+    auto drain = [&](auto i0_tag) __attribute__((always_inline)) {
+      constexpr int i0 = decltype(i0_tag)::value;
 #pragma unroll
       for (int i = 0; i < H; ++i)
 #pragma unroll
@@ -741,26 +745,38 @@ __global__ __launch_bounds__(256 * WM) void prefill_w_kernel(Args a) {
           if constexpr (Args::kGated) store_part(a.fin, part, a.m_first + m, n_lane + a.fin.out_n, a.N, sums_at(rr, 32 + lc));
         }
       } else {
+        if (shaped) {
 #pragma unroll 1
-        for (int t1 = 0; t1 < kPasses; t1 += kAhead) {
-#pragma unroll
-          for (int t = 0; t < kAhead; ++t) {
-            const int rr = (t1 + t) * kRowsAPass + lr, m = row0 + (t0 + t1 + t) * kRowsAPass;
-            const f32x4 r = residual_of(res[t]);
-            const float f = scale[t];
-            ask(t0 + t1 + t + kAhead, res[t], scale[t]);  // past the last row: that row's
+          for (int t = 0; t < kPasses; ++t) {
+            const int rr = t * kRowsAPass + lr;
+            const float f = scale_at(a.fin, a.m_first + min(row0 + (t0 + t) * kRowsAPass, a.M - 1));
             f32x4 up = {0, 0, 0, 0};
             if constexpr (Args::kGated) up = sums_at(rr, 32 + lc);
-            const f32x4 v = finish_values(a.fin, sums_at(rr, lc), up, f, bias, bias_up, r);
-            if (m < a.M && inside) store_four(a.fin, a.m_first + m, n_lane, v);
+            *reinterpret_cast<f32x4 *>(high + rr * SL + lc) = shape_values(a.fin, sums_at(rr, lc), up, f, bias, bias_up);
           }
+        }
+#pragma unroll
+        for (int t = 0; t < kPasses; ++t) {
+          const int rr = t * kRowsAPass + lr, m = row0 + (t0 + t) * kRowsAPass;
+          f32x4 v = shaped ? *reinterpret_cast<const f32x4 *>(high + rr * SL + lc) : sums_at(rr, lc);
+          const f32x4 r = residual_of(res[t]);
+          const float f = scale[t];
+          if (i0 + H < IM) ask(t0 + t + kPasses, res[t], scale[t]);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) v[q] = (shaped ? v[q] : __builtin_fmaf(v[q], f, bias[q])) + r[q];
+          if (m < a.M && inside) store_four(a.fin, a.m_first + m, n_lane, v);
         }
       }
       // the slab is rewritten by the next row blocks
       __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
       __builtin_amdgcn_wave_barrier();
       __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
-    }
+    };
+    drain(std::integral_constant<int, 0>{});
+    drain(std::integral_constant<int, H>{});
+    drain(std::integral_constant<int, 2 * H>{});
+    drain(std::integral_constant<int, 3 * H>{});
+    static_assert(IM == 4 * H, "four slabs");
     return;
   }
 #pragma unroll
