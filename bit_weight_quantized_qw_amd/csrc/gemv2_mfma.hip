@@ -49,6 +49,7 @@
 #include <type_traits>
 #include <vector>
 
+#include "linear.h"
 #include "qw_internal.h"
 
 namespace qw {
@@ -102,6 +103,11 @@ struct Args {
   int swiglu;         // 1: one merged gate/up matrix (m[0], 2I rows: gate
                       // rows 0..I-1, up rows I..2I-1, I % 16 == 0); y gets
                       // silu(gate) * up, I values per batch row
+};
+
+// A product of qgemm_linear: what stands behind the sums goes with the launch.
+struct ArgsLinear : Args {
+  Finish fin;
 };
 
 // SiLU of the gate projection's output, g * sigmoid(g), in fp32.
@@ -277,8 +283,8 @@ __device__ inline T sel4(int i, T v0, T v1, T v2, T v3) {
 // per group sum x q = 2 (P_lo + 4 P_hi) - 8 X_g. x limbs are in element
 // order.
 template <int B, int P, bool MULTI, bool XC = false, bool XR = true, int NT = kThreads, bool SW = false,
-          bool I4 = false>
-__device__ __forceinline__ void body(const Args &a, const int bid, uint8_t *lds) {
+          bool I4 = false, class ArgsT = Args>
+__device__ __forceinline__ void body(const ArgsT &a, const int bid, uint8_t *lds) {
   static_assert(!I4 || (!MULTI && !SW && !XC), "INT4 runs single-matrix launches");
   using SlotT = typename std::conditional<I4, Slot4, Slot>::type;
   constexpr int NW = NT / 64;
@@ -755,6 +761,17 @@ __device__ __forceinline__ void body(const Args &a, const int bid, uint8_t *lds)
     }
   };
 
+  // qgemm_linear: what this thread's output adds, asked for before the products
+  constexpr bool kLinear = std::is_same<ArgsT, ArgsLinear>::value;
+  [[maybe_unused]] float early_bias = 0.0f, early_residual = 0.0f;
+  if constexpr (kLinear) {
+    const int row = t0 * 16 + tid / B;
+    if (tid < (t1 - t0) * 16 * B && row < M.N) {
+      if (a.fin.bias) early_bias = load_any(a.fin.bias, row, a.fin.bias_dtype);
+      if (a.fin.residual) early_residual = load_any(a.fin.residual, (size_t)(tid - tid / B * B) * M.N + row, a.fin.residual_dtype);
+    }
+  }
+
   // Rounds of P steps: every round but the last refills each slot after
   // consuming it (unconditionally, so the waits count exactly; a refill past
   // the end reads through a zero-size descriptor); the last round only
@@ -826,6 +843,13 @@ __device__ __forceinline__ void body(const Args &a, const int bid, uint8_t *lds)
     float v = 0.0f;
     for (int sp = 0; sp < W; ++sp) v += parts[((size_t)(tl * W + sp) * 16 + jj) * B + b];
     const size_t off = (size_t)b * M.N + row;
+    if constexpr (kLinear) {
+      if (t == tid)
+        finish_one(a.fin, b, row, v, early_bias, early_residual);
+      else
+        finish_one(a.fin, b, row, v);
+      continue;
+    }
     if (XC) {  // written through to memory (y is a later stage's x)
       const auto ry = rsrc(M.y, (uint32_t)((size_t)B * M.N * (a.f32out ? 4 : 2)));
       if (a.f32out)
@@ -852,6 +876,13 @@ template <int B, bool XR>
 __global__ __launch_bounds__(kThreads) void kernel_int4(Args a) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   body<B, 3, false, false, XR, kThreads, false, true>(a, (int)blockIdx.x, lds);
+}
+
+// Either with what stands behind the sums of qgemm_linear.
+template <int B, bool I4>
+__global__ __launch_bounds__(kThreads) void kernel_linear(ArgsLinear a) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  body<B, 3, false, false, true, kThreads, false, I4>(a, (int)blockIdx.x, lds);
 }
 
 // ---------------------------------------------------------------------------
@@ -1450,6 +1481,36 @@ qw_status launch_int4(const qw_weight &w, const uint16_t *x, int B, void *y, boo
     b0 += bs;
   }
   return QW_OK;
+}
+
+template <int B, bool I4>
+static qw_status launch_linear_b(const ArgsLinear &a, int grid, size_t lds, hipStream_t s) {
+  if (lds > 64 * 1024)
+    QW_HIP_TRY(hipFuncSetAttribute(reinterpret_cast<const void *>(&kernel_linear<B, I4>),
+                                   hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds));
+  QW_HIP_TRY(qw::launch(kernel_linear<B, I4>, grid, kThreads, lds, s, a));
+  return QW_OK;
+}
+
+qw_status launch_linear(const qw_weight &w, const uint16_t *x, int M, const Finish &fin, int cus, hipStream_t s) {
+  const bool i4 = w.format == QW_FMT_INT4_G32;
+  if (M < 1 || M > (i4 ? 1 : 3)) return QW_ERR_UNSUPPORTED;
+  ArgsLinear a{};
+  int grid = 0;
+  void *ys[1] = {fin.Y};
+  QW_TRY(plan(&w, 1, x, ys, true, cus, a, grid, 1 << 30, kThreads, false, M));
+  if (i4) {  // anchors: the first n_out positions
+    a.m[0].mask = nullptr;
+    a.m[0].idx = nullptr;
+  }
+  int xr = 1, bmax = 0;
+  if (unsplit_slices(a, M, &xr, &bmax) != 1 || !xr) return QW_ERR_UNSUPPORTED;
+  a.xraw = xr;
+  a.fin = fin;
+  const size_t lds = lds_layout(M, w.K, a.xo_len, a.units_max, a.xraw).total;
+  if (i4) return launch_linear_b<1, true>(a, grid, lds, s);
+  return M == 1 ? launch_linear_b<1, false>(a, grid, lds, s)
+                : M == 2 ? launch_linear_b<2, false>(a, grid, lds, s) : launch_linear_b<3, false>(a, grid, lds, s);
 }
 
 }  // namespace gemv2m

@@ -24,6 +24,9 @@
 // and the lane's replica offset to byte 0.
 #include <stdlib.h>
 
+#include <type_traits>
+
+#include "linear.h"
 #include "qw_internal.h"
 
 namespace qw {
@@ -38,6 +41,10 @@ struct ArgsNf4 {
   void *y;                // [B][N]
   int N, K, rows_per_wg, W, f32out;
   float L[16];             // NF4 levels
+};
+
+struct ArgsNf4Linear : ArgsNf4 {
+  Finish fin;
 };
 
 __device__ inline float dot2(uint32_t a, uint32_t b, float c) {
@@ -85,8 +92,11 @@ __device__ inline float2 pair_at(const char *tab, uint32_t byte_off) {
 }
 
 // LDS: pair table (static, 64 KB) | x uint32 [B][K/2] | parts float [rows_per_wg][W][B]
-template <int B, int UW, int P>
-__global__ __launch_bounds__(kThreads) void gemv_nf4_kernel(ArgsNf4 a) {
+// ArgsNf4Linear: with what stands behind the sums of qgemm_linear (their rows
+// all go through parts, whose last step has the threads side by side).
+template <int B, int UW, int P, class ArgsT = ArgsNf4>
+__global__ __launch_bounds__(kThreads) void gemv_nf4_kernel(ArgsT a) {
+  constexpr bool kLinear = std::is_same<ArgsT, ArgsNf4Linear>::value;
   __shared__ __attribute__((aligned(16))) char pair_tab[256 * kPairStride];
   extern __shared__ __attribute__((aligned(16))) uint32_t lds[];
   uint32_t *xl = lds;
@@ -251,7 +261,7 @@ __global__ __launch_bounds__(kThreads) void gemv_nf4_kernel(ArgsNf4 a) {
     for (int b = 0; b < B; ++b) {
       const float v = wave_sum_to_lane63(acc[b]);
       if (lane == 63) {
-        if (W == 1) {
+        if (W == 1 && !kLinear) {
           const size_t off = (size_t)b * a.N + rr;
           if (a.f32out)
             reinterpret_cast<float *>(a.y)[off] = v;
@@ -263,6 +273,17 @@ __global__ __launch_bounds__(kThreads) void gemv_nf4_kernel(ArgsNf4 a) {
       }
     }
   };
+
+  // qgemm_linear: what this thread's output adds, asked for before the products
+  [[maybe_unused]] float early_bias = 0.0f, early_residual = 0.0f;
+  if constexpr (kLinear) {
+    const int rl = (int)threadIdx.x / B;
+    if ((int)threadIdx.x < (g1 - g0) * B) {
+      if (a.fin.bias) early_bias = load_any(a.fin.bias, g0 + rl, a.fin.bias_dtype);
+      if (a.fin.residual)
+        early_residual = load_any(a.fin.residual, (size_t)((int)threadIdx.x - rl * B) * a.N + g0 + rl, a.fin.residual_dtype);
+    }
+  }
 
   // rounds of P rows; all but the last refill each slot after using it
   const int n_rows = r1 - r0;
@@ -280,7 +301,7 @@ __global__ __launch_bounds__(kThreads) void gemv_nf4_kernel(ArgsNf4 a) {
   for (int i = 0; i < P; ++i)
     if (r + i < r1) compute(ring[i], r + i);
 
-  if (W > 1) {
+  if (W > 1 || kLinear) {
     __syncthreads();
     const int nrows = g1 - g0;
     for (int t = threadIdx.x; t < nrows * B; t += kThreads) {
@@ -288,6 +309,13 @@ __global__ __launch_bounds__(kThreads) void gemv_nf4_kernel(ArgsNf4 a) {
       float v = 0.0f;
       for (int i = 0; i < W; ++i) v += parts[(rl * W + i) * B + b];
       const size_t off = (size_t)b * a.N + (g0 + rl);
+      if constexpr (kLinear) {
+        if (t == (int)threadIdx.x)
+          finish_one(a.fin, b, g0 + rl, v, early_bias, early_residual);
+        else
+          finish_one(a.fin, b, g0 + rl, v);
+        continue;
+      }
       if (a.f32out)
         reinterpret_cast<float *>(a.y)[off] = v;
       else
@@ -322,7 +350,45 @@ qw_status launch_b(const ArgsNf4 &a, int B, int UW, bool deep, int grid, size_t 
   return launch_p<4, 1>(a, deep, grid, lds, s);
 }
 
+template <int UW>
+qw_status launch_linear_uw(const ArgsNf4Linear &a, int grid, size_t lds, hipStream_t s) {
+  constexpr auto kernel = gemv_nf4_kernel<1, UW, 3, ArgsNf4Linear>;
+  if (lds > 64 * 1024)
+    QW_HIP_TRY(hipFuncSetAttribute(reinterpret_cast<const void *>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds));
+  QW_HIP_TRY(launch(kernel, grid, kThreads, lds, s, a));
+  return QW_OK;
+}
+
 }  // namespace
+
+qw_status launch_linear_gemv_nf4(const qw_weight &w, const uint16_t *x, const Finish &fin, int cus, hipStream_t s) {
+  // one row, planned as qgemv_nf4 plans it
+  const int K = w.K, NH = K / 32;
+  int W = 1;
+  while (W < 8 && W * 64 * 4 < NH) W *= 2;
+  const int UW = (NH + 64 * W - 1) / (64 * W);
+  const int rpg = (int)max(1L, ((long)w.N + cus - 1) / cus);
+  const int grid = (w.N + rpg - 1) / rpg;
+  const size_t lds = (size_t)K * 2 + 4 * (size_t)rpg * W;
+  if (UW > 4 || lds + 256 * kPairStride > 160 * 1024 || (K / 8 + kThreads - 1) / kThreads > kXLoads) return QW_ERR_UNSUPPORTED;
+  ArgsNf4Linear a{};
+  a.codes = reinterpret_cast<const uint32_t *>(w.codes);
+  a.absmax = reinterpret_cast<const float *>(w.scales);
+  a.x = x;
+  a.y = fin.Y;
+  a.N = w.N;
+  a.K = K;
+  a.rows_per_wg = rpg;
+  a.W = W;
+  const float *lv = nf4_levels_host();
+  for (int i = 0; i < 16; ++i) a.L[i] = lv[i];
+  a.fin = fin;
+  if (UW == 1) return launch_linear_uw<1>(a, grid, lds, s);
+  if (UW == 2) return launch_linear_uw<2>(a, grid, lds, s);
+  if (UW == 3) return launch_linear_uw<3>(a, grid, lds, s);
+  return launch_linear_uw<4>(a, grid, lds, s);
+}
+
 }  // namespace qw
 
 extern "C" qw_status qgemv_nf4(const qw_weight *w, const void *x, int B, void *y,

@@ -132,6 +132,20 @@ __device__ inline f32x4 residual_at(const Finish &a, int m, int n) {
   return a.residual ? load_four(a.residual, (size_t)m * a.out_n + n, a.residual_dtype, a.out_n - n, a.out_n % 4 == 0) : f32x4{0, 0, 0, 0};
 }
 
+// All of it for one sum, column n of row m (not gated).
+__device__ inline void finish_one(const Finish &a, int m, int n, float v, float bias, float residual) {
+  v = activate(f32x4{v * scale_at(a, m) + bias, 0, 0, 0}, a.act)[0] + residual;
+  const size_t o = (size_t)m * a.out_n + n;
+  if (a.y_dtype == QW_DT_F32)
+    reinterpret_cast<float *>(a.Y)[o] = v;
+  else
+    reinterpret_cast<uint16_t *>(a.Y)[o] = (uint16_t)out_bits(v, a.y_dtype);
+}
+__device__ inline void finish_one(const Finish &a, int m, int n, float v) {
+  finish_one(a, m, n, v, a.bias ? load_any(a.bias, n, a.bias_dtype) : 0.0f,
+             a.residual ? load_any(a.residual, (size_t)m * a.out_n + n, a.residual_dtype) : 0.0f);
+}
+
 // Four sums of a part of K: columns n.. of row m, those below `end`.
 __device__ inline void store_part(const Finish &a, int part, int m, int n, int end, f32x4 v) {
   float *const o = a.partial + ((size_t)part * a.M + m) * a.N + n;
@@ -217,10 +231,20 @@ __device__ inline uint32_t one_as_16(const void *p, size_t element) {
   }
 }
 
-// The narrow kernel of one format (linear_narrow_*.hip); row_blocks: 16-row
-// blocks of a tile.
+// The decode GEMVs with what stands behind the sums in their epilogue, fp16
+// activations, not gated: 2-bit up to three rows and INT4 one row on the matrix
+// cores (gemv2_mfma.hip), NF4 one row (gemv_nf4.hip). QW_ERR_UNSUPPORTED
+// (nothing enqueued) where the shape does not fit them in one pass.
+namespace gemv2m {
+qw_status launch_linear(const qw_weight &w, const uint16_t *x, int M, const Finish &fin, int cus, hipStream_t s);
+}
+qw_status launch_linear_gemv_nf4(const qw_weight &w, const uint16_t *x, const Finish &fin, int cus, hipStream_t s);
+
+// The narrow kernel of one format (linear_narrow_*.hip): tiles of 16 MR rows (MR
+// = 0: of four) times 16 SUB columns by W waves.
+constexpr int narrow_shape(int MR, int SUB, int W) { return MR * 10000 + SUB * 100 + W; }
 template <int FMT>
-qw_status launch_linear_narrow(const LinearArgs &a, int row_blocks, hipStream_t s);
+qw_status launch_linear_narrow(const LinearArgs &a, int shape, hipStream_t s);
 // The tall kernel of one format (linear_tall_*.hip): the first high_tiles tiles
 // of columns by 256 rows, the others by 128.
 constexpr int tall_columns(bool gated) { return gated ? 128 : 256; }  // columns of Y of a tile

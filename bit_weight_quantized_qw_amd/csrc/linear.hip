@@ -26,12 +26,31 @@ __global__ __launch_bounds__(256) void join_kernel(Finish a, int parts, int col_
   store_four(a, m, n, shape_values(a, s, up, scale_at(a, m), bias_at(a, n), bias_up_at(a, n)) + residual_at(a, m, n));
 }
 
-// How a call runs: the narrow kernel with tiles of row_blocks blocks of 16 rows,
-// or (row_blocks 0) the tall one, the first high_tiles tiles of columns with
-// 256 rows; and the parts of K.
+// How a call runs: a decode GEMV, the narrow kernel with tiles of `shape`, or the
+// tall one, the first high_tiles tiles of columns with 256 rows; and the parts
+// of K.
+enum class Kernel { kGemv, kNarrow, kTall };
 struct Plan {
-  int row_blocks, high_tiles, parts;
+  Kernel kernel;
+  int shape, high_tiles, parts;
 };
+
+// Tile and waves of the narrow kernel for row blocks MR (0: up to four rows): as
+// many workgroups and waves as fill the CUs, more columns a wave where there
+// are enough of them (what a wave loads of X serves them all).
+int pick_narrow(int MR, int fmt, int out_n, int K, bool gated) {
+  const int blocks = (out_n + 15) / 16 * (gated ? 2 : 1), chunks = (K + 255) / 256;
+  if (MR == 0) {
+    if (fmt == QW_FMT_INT4_G32) MR = 1;  // no quicker for it
+  }
+  if (MR == 0) {
+    if (blocks <= 400 && !gated && chunks <= 48) return narrow_shape(0, 1, 8);
+    const int waves = 4200 / (blocks / 2 + 1);
+    return narrow_shape(0, 2, waves >= 16 ? 16 : waves >= 8 ? 8 : 4);
+  }
+  if (blocks < 600) return narrow_shape(MR, 2, 8);
+  return narrow_shape(MR, 4, MR == 1 && blocks / 4 > 300 ? 4 : 8);
+}
 
 // Column tiles by 256 rows: whole rounds over the CUs, and the rest by tiles of
 // 128 rows, two workgroups a CU, in place of a round that fills few of them.
@@ -52,21 +71,26 @@ int pick_high_tiles(int M, int nt) {
   return best_n;
 }
 
-Plan make_plan(int fmt, int M, int N, int K, bool gated) {
-  Plan p{0, 0, 1};
+// gemv: the call is one that a decode GEMV takes (fp16 activations, not gated).
+Plan make_plan(const qw_weight &w, int M, bool gated, bool gemv) {
+  const int fmt = w.format, N = w.N, K = w.K, out_n = gated ? N / 2 : N;
+  Plan p{Kernel::kNarrow, 0, 0, 1};
   const int forced = tune(QW_TUNE_LINEAR_ROW_BLOCKS);
-  const int blocks = forced > 0 ? forced : M <= 16 ? 1 : M <= 64 ? 2 : 16;
-  if (blocks < 8) {
-    p.row_blocks = blocks;
-  } else {
-    const int cols = tall_columns(gated), nt = ((gated ? N / 2 : N) + cols - 1) / cols;
+  const int most_gemv = fmt == QW_FMT_2BIT_G32 ? 3 : 1;
+  if (gemv && M <= most_gemv && forced <= 0) p.kernel = Kernel::kGemv;
+  if (forced >= 8 || (forced <= 0 && M > 64)) {
+    p.kernel = Kernel::kTall;
+    const int cols = tall_columns(gated), nt = (out_n + cols - 1) / cols;
     p.high_tiles = forced > 0 ? (forced >= 16 ? nt : 0) : pick_high_tiles(M, nt);
     if (p.high_tiles == 0) {
       const long long tiles = (long long)((M + 127) / 128) * nt;
       while (p.parts < 8 && tiles * p.parts * 2 <= 512 && K / 64 / (p.parts * 2) >= 8) p.parts *= 2;
     }
+  } else {
+    const int MR = forced > 0 ? (forced == 4 ? 0 : forced) : M <= 4 ? 0 : M <= 16 ? 1 : 2;
+    p.shape = pick_narrow(MR, fmt, out_n, K, gated);
   }
-  const int parts = tune(QW_TUNE_LINEAR_PARTS), step = p.row_blocks ? 256 : 64;
+  const int parts = tune(QW_TUNE_LINEAR_PARTS), step = p.kernel == Kernel::kTall ? 64 : 256;
   if (parts > 0) p.parts = parts < K / step ? parts : K / step > 1 ? K / step : 1;
   return p;
 }
@@ -79,8 +103,8 @@ bool takes(const qw_weight *w, int M) {
 
 template <int FMT>
 qw_status run(const LinearArgs &a, const Plan &p, hipStream_t s) {
-  if (p.row_blocks == 0) return launch_linear_tall<FMT>(a, p.high_tiles, s);
-  return launch_linear_narrow<FMT>(a, p.row_blocks, s);
+  if (p.kernel == Kernel::kTall) return launch_linear_tall<FMT>(a, p.high_tiles, s);
+  return launch_linear_narrow<FMT>(a, p.shape, s);
 }
 
 }  // namespace
@@ -92,7 +116,7 @@ size_t qw_linear_workspace_bytes(const qw_weight *w, int M) {
   if (!qw::takes(w, M)) return 0;
   int parts = 1;  // gated or not
   for (int gated = 0; gated < 2; ++gated) {
-    const qw::Plan p = qw::make_plan(w->format, M, w->N, w->K, gated != 0);
+    const qw::Plan p = qw::make_plan(*w, M, gated != 0, false);
     if (p.parts > parts) parts = p.parts;
   }
   return parts > 1 ? (size_t)parts * (size_t)M * (size_t)w->N * sizeof(float) : 0;
@@ -122,8 +146,9 @@ qw_status qgemm_linear(const qw_weight *w, const void *X, qw_dtype x_dtype, cons
   const size_t need = qw_linear_workspace_bytes(w, M);
   if (need && (!workspace || workspace_bytes < need)) return QW_ERR_INVALID_ARG;
   if (need && !aligned16(workspace)) return QW_ERR_ALIGNMENT;
-  QW_TRY(current_device(nullptr));
-  const Plan plan = make_plan(w->format, M, w->N, w->K, ep->gated != 0);
+  int cus = 0;
+  QW_TRY(current_device(&cus));
+  Plan plan = make_plan(*w, M, ep->gated != 0, x_dtype == QW_DT_F16 && !ep->gated);
   LinearArgs a{};
   a.X = X;
   a.codes = w->codes;
@@ -144,6 +169,13 @@ qw_status qgemm_linear(const qw_weight *w, const void *X, qw_dtype x_dtype, cons
   const float *L = nf4_levels_host();
   for (int i = 0; i < 16; ++i) a.nf4[i] = L[i];
   const hipStream_t s = as_stream(stream);
+  if (plan.kernel == Kernel::kGemv) {
+    const uint16_t *x = reinterpret_cast<const uint16_t *>(X);
+    const qw_status st = w->format == QW_FMT_NF4_B64 ? launch_linear_gemv_nf4(*w, x, a.fin, cus, s)
+                                                     : gemv2m::launch_linear(*w, x, M, a.fin, cus, s);
+    if (st != QW_ERR_UNSUPPORTED) return st;
+    plan = make_plan(*w, M, gated, false);
+  }
   if (w->format == QW_FMT_2BIT_G32)
     QW_TRY(run<QW_FMT_2BIT_G32>(a, plan, s));
   else if (w->format == QW_FMT_INT4_G32)

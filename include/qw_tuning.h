@@ -45,8 +45,9 @@ typedef enum {
    * 4 the wide one with tiles of that many 16-row blocks, 8 or 16 the tall
    * one where it takes the call (else 4). */
   QW_TUNE_EXPERTS_ROW_BLOCKS = 7,
-  /* qgemm_linear: -1 / 0 automatic, 1, 2 or 4 the narrow kernel with tiles of
-   * that many 16-row blocks, 8 or 16 the tall one. */
+  /* qgemm_linear: -1 / 0 automatic, 1 or 2 the narrow kernel with tiles of
+   * that many 16-row blocks, 4 the narrow one with tiles of four rows, 8 or 16
+   * the tall one with tiles of that many 16-row blocks. */
   QW_TUNE_LINEAR_ROW_BLOCKS = 8,
   /* qgemm_linear: -1 / 0 automatic, n >= 1 that many parts of K (at most one a
    * step of 64, narrow tiles of 256). qw_linear_workspace_bytes follows it. */

@@ -70,8 +70,8 @@ def test_rows(fmt, M):
     case(fmt, M, 512, 96, "f16", "f32", seed=M)
 
 
-# every kernel on the same shapes: 16-row blocks of a tile, parts of K
-PATHS = [(1, 1), (1, 3), (2, 1), (2, 4), (8, 1), (8, 3), (16, 1), (16, 2)]
+# every kernel on the same shapes: 16-row blocks of a tile (4: four rows), parts of K
+PATHS = [(4, 1), (4, 2), (1, 1), (1, 3), (2, 1), (2, 4), (8, 1), (8, 3), (16, 1), (16, 2)]
 
 
 @pytest.mark.parametrize("blocks,parts", PATHS)
@@ -94,6 +94,17 @@ def test_every_kernel_and_epilogue(tune, blocks, parts, gated, N):
     for y in ("f16", "bf16", "f32"):
         case("int4", 100, 512, N, "bf16", y, 9, "f32", "silu", gated, "bf16", seed=N, rounded=blocks >= 8)
     case("2bit", 270, 320, N + (0 if gated else 1), "i8", "f16", 11, "f16", "gelu", gated, "f16", seed=N + 1, rounded=blocks >= 8)
+
+
+@pytest.mark.parametrize("fmt,anchors", [("2bit", 0), ("2bit", 40), ("nf4", 0), ("int4", 0), ("int4", 9)])
+@pytest.mark.parametrize("M", [1, 2, 3, 4])
+@pytest.mark.parametrize("N,K", [(1000, 512), (5120, 1024), (30, 2560), (11000, 512), (9000, 576)])
+def test_few_rows_fp16(fmt, anchors, M, N, K):
+    """Single tokens: the decode GEMVs' shapes and those that they do not take, with every
+    epilogue part."""
+    case(fmt, M, K, N, "f16", "f32", anchors, "f16", "gelu_tanh", False, "bf16", seed=M + N)
+    case(fmt, M, K, N, "f16", "f16", anchors, None, None, False, "f16", seed=M + N)
+    case(fmt, M, K, N, "f16", "f16", anchors, "f32", "silu", True, "f32", seed=M + N)
 
 
 def test_fp16_weights_of_any_size_keep_their_bits(tune):
