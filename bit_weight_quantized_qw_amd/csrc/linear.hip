@@ -71,24 +71,68 @@ int pick_high_tiles(int M, int nt) {
   return best_n;
 }
 
+// Estimated time of the tall kernel, us, with every column tile 256 (high) or
+// 128 rows high and K in `parts`: a start, the steps of 64 elements one behind
+// another, slower where two workgroups share a CU or follow each other, and the
+// sum over the parts. A step of a workgroup alone on its CU is bound by the
+// issue of its own waves (products, and decoding beside them), not by memory:
+// loads three steps ahead instead of one left it as it was. And of the narrow
+// kernel with tiles of 32 rows: what its products take. Measured / estimated
+// (bf16; with anchors int8), M x N x K: narrow, and by 128 rows with K in 1, 4
+// and 8 parts:
+//   2-bit, anchors 100 x  5120 x  5120    70/83     108/114     40/43      31/33
+//   2-bit, anchors 100 x  8192 x 28672   399/409    560/592    155/165     95/97
+//   2-bit, anchors 333 x  1501 x  2048    36/32      59/52      33/27      35/25
+//   2-bit          100 x  5120 x  5120    48/50      81/86      32/36      25/30
+//   2-bit          100 x  8192 x 28672   253/309    389/436    115/125     77/77
+//   2-bit          333 x  1501 x  2048    27/22      45/40      27/25      30/24
+//   NF4            100 x  5120 x  5120    53/50     156/162     59/55      44/39
+//   NF4            100 x  8192 x 28672   284/309    802/861    230/232    138/130
+//   NF4            333 x  1501 x  2048    30/22      83/71      46/32      45/28
+//   INT4           100 x  5120 x  5120    49/50     107/108     38/42      28/33
+//   INT4           100 x  8192 x 28672   266/309    562/557    158/156     95/92
+//   INT4           333 x  1501 x  2048    26/22      52/49      29/27      31/25
+double tall_time(int fmt, bool anchors, int M, int nt, int N, int K, bool high, int parts) {
+  const int f = fmt == QW_FMT_2BIT_G32 ? anchors : fmt == QW_FMT_NF4_B64 ? 2 : 3;
+  constexpr double kStep[4][2] = {{0.95, 1.35}, {1.3, 1.9}, {1.9, 2.8}, {1.22, 1.65}};
+  const double steps = ceil((double)(K / 64) / parts);
+  const double groups = (double)((M + (high ? 255 : 127)) / (high ? 256 : 128)) * nt * parts;
+  const double rounds = high ? ceil(groups / 256) : groups <= 256 ? 1.0 : 1.7 * fmax(1.0, groups / 512 + 0.2);
+  return 10 + steps * kStep[f][high] * rounds + (parts > 1 ? 4 + 8.0 * parts * M * N / 5.2e6 : 0);
+}
+double narrow_time(int fmt, bool anchors, int M, int N, int K, int shape) {
+  const double macs = (double)((M + 31) / 32 * 32) * N * K;
+  const bool two = shape / 100 % 100 == 2 && K < 8192;  // 16-column blocks of a wave
+  return 8 + macs / (fmt == QW_FMT_2BIT_G32 && anchors ? (two ? 45e6 : 75e6) : two ? 80e6 : 100e6);
+}
+
 // gemv: the call is one that a decode GEMV takes (fp16 activations, not gated).
 Plan make_plan(const qw_weight &w, int M, bool gated, bool gemv) {
   const int fmt = w.format, N = w.N, K = w.K, out_n = gated ? N / 2 : N;
   Plan p{Kernel::kNarrow, 0, 0, 1};
   const int forced = tune(QW_TUNE_LINEAR_ROW_BLOCKS);
   const int most_gemv = fmt == QW_FMT_2BIT_G32 ? 3 : 1;
+  const int cols = tall_columns(gated), nt = (out_n + cols - 1) / cols;
   if (gemv && M <= most_gemv && forced <= 0) p.kernel = Kernel::kGemv;
-  if (forced >= 8 || (forced <= 0 && M > 64)) {
+  const int MR = forced > 0 && forced < 8 ? (forced == 4 ? 0 : forced) : M <= 4 ? 0 : M <= 16 ? 1 : 2;
+  p.shape = pick_narrow(MR, fmt, out_n, K, gated);
+  if (forced >= 8) {
     p.kernel = Kernel::kTall;
-    const int cols = tall_columns(gated), nt = (out_n + cols - 1) / cols;
-    p.high_tiles = forced > 0 ? (forced >= 16 ? nt : 0) : pick_high_tiles(M, nt);
-    if (p.high_tiles == 0) {
-      const long long tiles = (long long)((M + 127) / 128) * nt;
-      while (p.parts < 8 && tiles * p.parts * 2 <= 512 && K / 64 / (p.parts * 2) >= 8) p.parts *= 2;
+    p.high_tiles = forced >= 16 ? nt : 0;
+  } else if (forced <= 0 && M > 32) {
+    double least = narrow_time(fmt, w.n_out > 0, M, N, K, p.shape);
+    auto consider = [&](double t, int high_tiles, int parts) {
+      if (t >= least) return;
+      least = t;
+      p.kernel = Kernel::kTall;
+      p.high_tiles = high_tiles;
+      p.parts = parts;
+    };
+    for (int parts = 1; parts <= 16 && K / 64 / parts >= 2; parts *= 2) {
+      consider(tall_time(fmt, w.n_out > 0, M, nt, N, K, false, parts), 0, parts);
+      consider(tall_time(fmt, w.n_out > 0, M, nt, N, K, true, parts), nt, parts);
     }
-  } else {
-    const int MR = forced > 0 ? (forced == 4 ? 0 : forced) : M <= 4 ? 0 : M <= 16 ? 1 : 2;
-    p.shape = pick_narrow(MR, fmt, out_n, K, gated);
+    if (p.kernel == Kernel::kTall && p.parts == 1) p.high_tiles = pick_high_tiles(M, nt);
   }
   const int parts = tune(QW_TUNE_LINEAR_PARTS), step = p.kernel == Kernel::kTall ? 64 : 256;
   if (parts > 0) p.parts = parts < K / step ? parts : K / step > 1 ? K / step : 1;

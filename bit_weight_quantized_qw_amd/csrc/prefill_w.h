@@ -371,7 +371,7 @@ __global__ __launch_bounds__(256 * WM) void prefill_w_kernel(Args a) {
         }
       }
     }
-    if constexpr (Args::kLinear) {  // and its anchors
+    if constexpr (Args::kLinear && FMT != QW_FMT_NF4_B64) {  // and its anchors
       for (int o = hk * 8; o < a.n_out; o += 16) {
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
@@ -571,25 +571,41 @@ __global__ __launch_bounds__(256 * WM) void prefill_w_kernel(Args a) {
   // ---- anchors: 64 channels a step, their X gathered into a buffer, their
   //      weights as the others enter ----
   if constexpr (Args::kLinear) {
-    if (a.n_out > 0 && part == a.parts - 1) {
-      for (int o0 = 0; o0 < a.n_out; o0 += BK) {
-#pragma unroll 1
-        for (int i = 0; i < IM; ++i) {
-          const int gm = min(m0 + xr + 32 * WM * i, a.M - 1);  // rows past M are not stored
-          u32x4 v = {0, 0, 0, 0};
+    // (the parts of K take the steps in turn)
+    if (FMT != QW_FMT_NF4_B64 && a.n_out > 0) {
+      [[maybe_unused]] const auto ri = pf_rsrc(a.idx, FMT == QW_FMT_2BIT_G32 ? (uint32_t)a.n_out * 4u : 0u);
+      const uint16_t *xrow[IM];
+#pragma unroll
+      for (int i = 0; i < IM; ++i)  // rows past M are not stored
+        xrow[i] = reinterpret_cast<const uint16_t *>(reinterpret_cast<const char *>(a.X) + (size_t)min(m0 + xr + 32 * WM * i, a.M - 1) * K * XB);
+      for (int o0 = part * BK; o0 < a.n_out; o0 += a.parts * BK) {
+        uint32_t at[8];
+        if (FMT == QW_FMT_2BIT_G32) {  // past the last: channel 0
+          const u32x4 lo = __builtin_amdgcn_raw_buffer_load_b128(ri, (o0 + xc) * 4, 0, 0);
+          const u32x4 hi = __builtin_amdgcn_raw_buffer_load_b128(ri, (o0 + xc) * 4 + 16, 0, 0);
 #pragma unroll
           for (int q = 0; q < 8; ++q) {
-            const int o = o0 + xc + q;
-            if (o < a.n_out) {
-              int k = o;
-              if (FMT == QW_FMT_2BIT_G32) {
-                k = a.idx[o];
-                if ((uint32_t)k >= (uint32_t)K) k = 0;
-              }
-              v[q >> 1] |= Args::one(a.X, (size_t)gm * K + k) << (16 * (q & 1));
-            }
+            at[q] = q < 4 ? lo[q & 3] : hi[q & 3];
+            if (at[q] >= (uint32_t)K) at[q] = 0;
           }
-          *reinterpret_cast<u32x4 *>(xs + 32 * WM * i * LDA) = v;
+        } else {
+#pragma unroll
+          for (int q = 0; q < 8; ++q) at[q] = (uint32_t)min(o0 + xc + q, a.n_out - 1);
+        }
+        uint32_t v[IM][8];  // all of a step's elements are on their way together
+#pragma unroll
+        for (int i = 0; i < IM; ++i)
+#pragma unroll
+          for (int q = 0; q < 8; ++q) v[i][q] = Args::one(xrow[i], at[q]);
+#pragma unroll
+        for (int i = 0; i < IM; ++i) {
+          u32x4 w;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint32_t lo = o0 + xc + 2 * q < a.n_out ? v[i][2 * q] : 0u, hi = o0 + xc + 2 * q + 1 < a.n_out ? v[i][2 * q + 1] : 0u;
+            w[q] = lo | (hi << 16);
+          }
+          *reinterpret_cast<u32x4 *>(xs + 32 * WM * i * LDA) = w;
         }
         __syncthreads();
 #pragma unroll 1
