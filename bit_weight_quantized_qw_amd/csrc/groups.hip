@@ -186,12 +186,19 @@ __device__ inline void topk_tokens(const RouteArgs &a, int t0, int count, int32_
 // experts: with the number of groups rounded up to a power of two, lane `sub`
 // belongs to group sub / P and holds the experts sub % P, sub % P + P, ... of
 // it, so a group's largest and second come from log2 P exchanges, and with
-// one group the layout is that of the top-k above. Choices are 64-bit
-// numbers: sigmoids of logits that differ in fp32 agree in fp32 as soon as
-// they come near 1, and a bias of 0.1 leaves scores of 1e-4 three digits. Each
-// round takes the largest choice (its pattern as an ordered integer) and then
-// the lowest expert that has it. The chosen experts' scores are computed again
-// from their logits, one a lane, rather than kept.
+// one group the layout is that of the top-k above.
+//
+// The order has to be that of 64-bit numbers: sigmoids of logits that differ in
+// fp32 agree in fp32 as soon as they come near 1, and a bias of 0.1 leaves
+// scores of 1e-4 three digits. So the choice is made in fp32 first, and where
+// two values that it depends on are nearer to each other than fp32 can tell
+// (kUnsure), it is made again in 64 bits: some tokens in a hundred with fp32
+// logits, all with equal choices. Without a bias a score's order is its logit's,
+// and only sums of two are ever unsure. 16384 tokens, 8 of 256 in 4 of 8 groups:
+// 39 us, all of it in 64 bits 52.
+//
+// The chosen experts' scores are computed again from their logits, one a lane
+// and in 64 bits, rather than kept.
 
 struct ScoredArgs {
   const void *logits;
@@ -214,6 +221,14 @@ __device__ inline double from_ordered64(unsigned long long k) {
   return __builtin_bit_cast(double, (k >> 63) ? (k & ~(1ull << 63)) : ~k);
 }
 
+// Order of a 16-bit logit (not NaN or -inf) as an integer of 16 bits, >= 1.
+template <int DT>
+__device__ inline uint32_t ordered16(float x) {
+  const uint32_t h = DT == QW_DT_BF16 ? __builtin_bit_cast(uint32_t, x) >> 16 : (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)x);
+  const uint32_t mag = h & 0x7FFFu;
+  return mag && (h & 0x8000u) ? 0x8000u - mag : 0x8000u + mag;
+}
+
 template <int DT>
 __device__ inline float logit_at(const void *p, size_t i) {
   if constexpr (DT == QW_DT_F32) return reinterpret_cast<const float *>(p)[i];
@@ -221,103 +236,265 @@ __device__ inline float logit_at(const void *p, size_t i) {
   return DT == QW_DT_BF16 ? __builtin_bit_cast(float, h << 16) : f16_bits_to_f32((uint16_t)h);
 }
 
-template <int DT, int L, int V>
-__device__ inline void choose_tokens(const ScoredArgs &a, int t0, int count, int32_t *sid) {
+// What the lanes of a token know of it. Lane `sub` holds the experts
+// first + v P of its group.
+template <int L, int V>
+struct TokenLanes {
+  int sub, P, group, first;
+  __device__ TokenLanes(const ScoredArgs &a) {
+    sub = threadIdx.x % L;
+    P = L;  // lanes of a group
+    while (L / P < a.groups) P /= 2;
+    group = sub / P;
+    first = group * a.group_size + sub % P;
+  }
+  __device__ bool has(const ScoredArgs &a, int v) const { return group < a.groups && v * P + sub % P < a.group_size; }
+};
+
+__device__ inline double score64(const ScoredArgs &a, float l, float most, double sum) {
+  return a.score == QW_ROUTE_SOFTMAX ? exp((double)l - (double)most) / sum : 1.0 / (1.0 + exp(-(double)l));
+}
+template <int L>
+__device__ inline double sum_of(double v) {
+#pragma unroll
+  for (int d = L / 2; d; d >>= 1) v += __shfl_xor(v, d, L);
+  return v;
+}
+// The sum of the exponentials of all of a token's logits.
+template <int L, int V>
+__device__ inline double sum64(const float (&x)[V], float most) {
+  double sum = 0.0;
+#pragma unroll
+  for (int v = 0; v < V; ++v) sum += x[v] > -INFINITY ? exp((double)x[v] - (double)most) : 0.0;
+  return sum_of<L>(sum);
+}
+
+// The choice in 64 bits: this lane's expert (lane j of the token keeps choice
+// j), -1 where there is none.
+template <int L, int V>
+__device__ inline int choose64(const ScoredArgs &a, const TokenLanes<L, V> &t, const float (&x)[V], const float (&bias)[V], float most) {
   typedef unsigned long long key_t;
-  const int sub = threadIdx.x % L;
-  int P = L;  // lanes of a group
-  while (L / P < a.groups) P /= 2;
-  const int group = sub / P;
-  for (int i = threadIdx.x / L; i < count; i += kThreads / L) {
+  const double sum = a.score == QW_ROUTE_SOFTMAX ? sum64<L>(x, most) : 1.0;
+  key_t key[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    key[v] = 0;
+    if (x[v] > -INFINITY) key[v] = ordered64(score64(a, x[v], most, sum) + (double)bias[v]);
+  }
+  if (a.top_groups < a.groups) {
+    key_t one = 0, two = 0;  // the group's largest and second
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      two = max(two, min(one, key[v]));
+      one = max(one, key[v]);
+    }
+    for (int d = t.P / 2; d; d >>= 1) {
+      const key_t f = __shfl_xor(one, d, L), s = __shfl_xor(two, d, L);
+      two = max(min(one, f), max(two, s));
+      one = max(one, f);
+    }
+    key_t value = one;
+    if (a.by == QW_GROUP_TOP2 && two) value = ordered64(from_ordered64(one) + from_ordered64(two));
+    int before = 0;
+    for (int g = 0; g < a.groups; ++g) {
+      const key_t o = __shfl(value, g * t.P, L);
+      before += o > value || (o == value && g < t.group);
+    }
+    if (before >= a.top_groups) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) key[v] = 0;
+    }
+  }
+  int id = -1;
+  for (int j = 0; j < a.k; ++j) {
+    key_t best = key[0];
+#pragma unroll
+    for (int v = 1; v < V; ++v) best = key[v] > best ? key[v] : best;
+    best = lanes_max<L>(best);
+    uint32_t at = 0;  // the inverted number of the lowest expert that has it
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (best && key[v] == best) at = max(at, ~(uint32_t)(t.first + v * t.P));
+    at = lanes_max<L>(at);
+    if (t.sub == j && best) id = (int)~at;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (~(uint32_t)(t.first + v * t.P) == at) key[v] = 0;
+  }
+  return id;
+}
+
+// How near two fp32 choices may lie and still be unsure. A sigmoid is off by
+// |l| s (1 - s) 2^-23 + s (1 - s) 2^-23 (the exponential's argument, rounded
+// twice, and its step) and two roundings of numbers up to 1: less than 3e-7. A
+// softmax's sum adds up to 16 roundings of itself: less than 1.2e-6. The bias's
+// addition rounds once more, and two values are compared.
+__device__ inline float unsure(const ScoredArgs &a, float c) {
+  return (a.score == QW_ROUTE_SIGMOID ? 8e-7f : 3e-6f) + 0x1p-22f * fabsf(c);
+}
+
+// The same with 32-bit keys; chosen[j] (LDS) receives choice j. Returns whether
+// it is the choice in 64 bits for sure.
+//
+// A round is a maximum over the lane's keys and the lanes, and the lane that has
+// it stores its number and clears it. Keys of 16-bit logits hold the inverted
+// number behind the logit, so no two are equal; equal keys of the other kinds
+// show in the count of what k rounds have cleared.
+template <int DT, int L, int V>
+__device__ inline bool choose32(const ScoredArgs &a, const TokenLanes<L, V> &t, const float (&x)[V], const float (&bias)[V], float most, int32_t *chosen) {
+  const bool sums = a.top_groups < a.groups && a.by == QW_GROUP_TOP2;
+  const bool scores = a.bias || sums;  // else the logits have the order
+  bool sure = true;
+  float c[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) c[v] = x[v];
+  if (scores) {
+    float inv = 1.0f;
+    if (a.score == QW_ROUTE_SOFTMAX) {
+      float sum = 0.0f;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        c[v] = x[v] > -INFINITY ? __expf(x[v] - most) : 0.0f;
+        sum += c[v];
+      }
+#pragma unroll
+      for (int d = L / 2; d; d >>= 1) sum += __shfl_xor(sum, d, L);
+      inv = 1.0f / sum;
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const float s = a.score == QW_ROUTE_SOFTMAX ? c[v] * inv : __frcp_rn(1.0f + __expf(-x[v]));
+      c[v] = x[v] > -INFINITY ? s + bias[v] : -INFINITY;
+    }
+  }
+  if (a.top_groups < a.groups) {
+    float one = -INFINITY, two = -INFINITY;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      two = fmaxf(two, fminf(one, c[v]));
+      one = fmaxf(one, c[v]);
+    }
+    for (int d = t.P / 2; d; d >>= 1) {
+      const float f = __shfl_xor(one, d, L), s = __shfl_xor(two, d, L);
+      two = fmaxf(fminf(one, f), fmaxf(two, s));
+      one = fmaxf(one, f);
+    }
+    const float value = sums && two > -INFINITY ? one + two : one;
+    const float near = scores ? 2.0f * unsure(a, value) : -1.0f;
+    int before = 0;
+    for (int g = 0; g < a.groups; ++g) {
+      const float o = __shfl(value, g * t.P, L);
+      before += o > value || (o == value && g < t.group);
+      // (a group that has no expert left is behind all others in any case)
+      if (g != t.group && value > -INFINITY && o > -INFINITY && !(fabsf(o - value) > near)) sure = false;
+    }
+    if (before >= a.top_groups) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) c[v] = -INFINITY;
+    }
+  }
+  // without a bias the order within the groups is the logits'
+  const bool unique = DT != QW_DT_F32 && !a.bias;
+  uint32_t key[V];
+  int left = 0;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const uint32_t o = ordered32(a.bias ? c[v] : c[v] > -INFINITY ? x[v] : -INFINITY);
+    key[v] = o;
+    if constexpr (DT != QW_DT_F32)
+      if (unique && o) key[v] = (ordered16<DT>(x[v]) << 16) | (0xFFFFu - (uint32_t)(t.first + v * t.P));
+    left += key[v] != 0;
+  }
+  if (t.sub < a.k) chosen[t.sub] = -1;
+  float last = INFINITY;
+  int taken = 0;
+  const int rounds = a.bias ? a.k + 1 : a.k;  // the first that is not chosen, too
+  for (int j = 0; j < rounds; ++j) {
+    uint32_t best = key[0];
+#pragma unroll
+    for (int v = 1; v < V; ++v) best = max(best, key[v]);
+    best = lanes_max<L>(best);
+    if (a.bias && best) {
+      const float value = from_ordered32(best);
+      if (!(last - value > unsure(a, value))) sure = false;  // j = 0: infinity, and NaN where the value is infinite too
+      last = value;
+    }
+    if (j == a.k || __all(best == 0)) break;
+    int at = -1;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const bool is = key[v] == best;
+      at = is ? v : at;
+      key[v] = is ? 0 : key[v];
+    }
+    if (best) {
+      ++taken;
+      if (at >= 0) chosen[j] = t.first + at * t.P;
+    }
+  }
+  if (!unique) {
+    int now = 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) now += key[v] != 0;
+    int gone = left - now;
+#pragma unroll
+    for (int d = L / 2; d; d >>= 1) gone += __shfl_xor(gone, d, L);
+    if (gone != taken) sure = false;
+  }
+  return sure;
+}
+
+template <int DT, int L, int V, int NT>
+__device__ inline void choose_tokens(const ScoredArgs &a, int t0, int count, int32_t *sid) {
+  const TokenLanes<L, V> lanes(a);
+  const int sub = lanes.sub;
+  constexpr int kSide = NT / L;  // tokens side by side
+  float next[V];
+  auto load = [&](int i) {
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      next[v] = i < count && lanes.has(a, v) ? logit_at<DT>(a.logits, (size_t)(t0 + i) * a.E + lanes.first + v * lanes.P) : -INFINITY;
+  };
+  load(threadIdx.x / L);
+  float bias[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) bias[v] = a.bias && lanes.has(a, v) ? a.bias[lanes.first + v * lanes.P] : 0.0f;
+  for (int i = threadIdx.x / L; i < count; i += kSide) {
     const int t = t0 + i;
     float x[V];
     float most = -INFINITY;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int in = v * P + sub % P;
-      x[v] = -INFINITY;
-      if (group < a.groups && in < a.group_size) {
-        const float l = logit_at<DT>(a.logits, (size_t)t * a.E + group * a.group_size + in);
-        if (l > -INFINITY) x[v] = l;  // NaN is taken as -inf
-      }
+      x[v] = next[v] > -INFINITY ? next[v] : -INFINITY;  // NaN is taken as -inf
       most = fmaxf(most, x[v]);
     }
-    double sum = 1.0;
-    if (a.score == QW_ROUTE_SOFTMAX) {
+    load(i + kSide);
+    const bool softmax = a.score == QW_ROUTE_SOFTMAX;
+    if (softmax) {
 #pragma unroll
       for (int d = L / 2; d; d >>= 1) most = fmaxf(most, __shfl_xor(most, d, L));
-      sum = 0.0;
-#pragma unroll
-      for (int v = 0; v < V; ++v) sum += x[v] > -INFINITY ? exp((double)x[v] - (double)most) : 0.0;
-#pragma unroll
-      for (int d = L / 2; d; d >>= 1) sum += __shfl_xor(sum, d, L);
     }
-    auto score_of = [&](float l) {
-      return a.score == QW_ROUTE_SOFTMAX ? exp((double)l - (double)most) / sum : 1.0 / (1.0 + exp(-(double)l));
-    };
-    key_t key[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      key[v] = 0;
-      if (x[v] > -INFINITY) {
-        const double bias = a.bias ? (double)a.bias[group * a.group_size + v * P + sub % P] : 0.0;
-        key[v] = ordered64(score_of(x[v]) + bias);
-      }
+    int32_t *const chosen = sid + i * a.k;
+    const bool sure = choose32<DT, L>(a, lanes, x, bias, most, chosen) && !(softmax && most == INFINITY);  // such a row has no scores
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+    __builtin_amdgcn_wave_barrier();
+    int id = sub < a.k ? chosen[sub] : -1;
+    if (__any(!sure)) {
+      id = choose64<L>(a, lanes, x, bias, most);
+      if (sub < a.k) chosen[sub] = id;
     }
-    if (a.top_groups < a.groups) {
-      key_t first = 0, second = 0;  // of the group's choices
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        second = max(second, min(first, key[v]));
-        first = max(first, key[v]);
-      }
-      for (int d = P / 2; d; d >>= 1) {
-        const key_t f = __shfl_xor(first, d, L), s = __shfl_xor(second, d, L);
-        second = max(min(first, f), max(second, s));
-        first = max(first, f);
-      }
-      key_t value = first;
-      if (a.by == QW_GROUP_TOP2 && second) value = ordered64(from_ordered64(first) + from_ordered64(second));
-      int before = 0;  // groups of a larger value, or an equal one and a lower number
-      for (int g = 0; g < a.groups; ++g) {
-        const key_t o = __shfl(value, g * P, L);
-        before += o > value || (o == value && g < group);
-      }
-      if (before >= a.top_groups) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) key[v] = 0;
-      }
-    }
-    int id = -1;  // lane j of the token keeps choice j
-    for (int j = 0; j < a.k; ++j) {
-      key_t best = key[0];
-#pragma unroll
-      for (int v = 1; v < V; ++v) best = key[v] > best ? key[v] : best;
-      best = lanes_max<L>(best);
-      uint32_t at = 0;  // the inverted number of the lowest expert that has it
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-        if (best && key[v] == best) at = max(at, ~(uint32_t)(group * a.group_size + v * P + sub % P));
-      at = lanes_max<L>(at);
-      if (sub == j && best) id = (int)~at;
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-        if (~(uint32_t)(group * a.group_size + v * P + sub % P) == at) key[v] = 0;
-    }
-    double w = 0.0;
-    if (id >= 0) w = score_of(logit_at<DT>(a.logits, (size_t)t * a.E + id));
+    // normalised weights do not need the sum over all experts
+    const double sum = softmax && !a.normalize ? sum64<L>(x, most) : 1.0;
+    const double w = id >= 0 ? score64(a, logit_at<DT>(a.logits, (size_t)t * a.E + id), most, sum) : 0.0;
     double factor = (double)a.scale;
     if (a.normalize) {
-      double total = w;
-#pragma unroll
-      for (int d = L / 2; d; d >>= 1) total += __shfl_xor(total, d, L);
+      const double total = sum_of<L>(w);
       factor = total > 0.0 ? factor / total : 0.0;
     }
     if (sub < a.k) {
       const size_t o = (size_t)t * a.k + sub;
       a.ids[o] = id;
       a.weights[o] = id >= 0 ? (float)(w * factor) : 0.0f;
-      if (sid) sid[i * a.k + sub] = id;
     }
   }
 }
@@ -340,10 +517,11 @@ constexpr size_t group_lds_bytes(int G) {
 }
 
 // Counts of the block's slots per group (G: none) into base.
+template <int NT = kThreads>
 __device__ inline void count_slots(const GroupLds &l, int slots, int G) {
-  for (int g = threadIdx.x; g <= G; g += kThreads) l.base[g] = 0;
+  for (int g = threadIdx.x; g <= G; g += NT) l.base[g] = 0;
   __syncthreads();
-  for (int i = threadIdx.x; i < slots; i += kThreads) {
+  for (int i = threadIdx.x; i < slots; i += NT) {
     const int id = l.sid[i];
     atomicAdd(&l.base[(uint32_t)id < (uint32_t)G ? id : G], 1);
   }
@@ -436,9 +614,10 @@ __device__ inline void group_alone(const GroupArgs &g, const GroupLds &l) {
   place_slots(l, g.n, 0, g.G, g.rows);
 }
 
+template <int NT = kThreads>
 __device__ inline void write_counts(const GroupArgs &g, const GroupLds &l, int slots) {
-  count_slots(l, slots, g.G);
-  for (int i = threadIdx.x; i < g.G; i += kThreads) g.counts[(size_t)blockIdx.x * g.G + i] = l.base[i];
+  count_slots<NT>(l, slots, g.G);
+  for (int i = threadIdx.x; i < g.G; i += NT) g.counts[(size_t)blockIdx.x * g.G + i] = l.base[i];
 }
 
 template <int DT, int L, int V>
@@ -456,19 +635,20 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a, GroupArgs 
     write_counts(g, l, count * a.k);
 }
 
-template <int DT, int L, int V>
-__global__ __launch_bounds__(kThreads) void scored_kernel(ScoredArgs a, GroupArgs g) {
+// NT: threads of a block; more than kThreads only where several blocks run.
+template <int DT, int L, int V, int NT>
+__global__ __launch_bounds__(NT) void scored_kernel(ScoredArgs a, GroupArgs g) {
   extern __shared__ int32_t smem[];
   const GroupLds l = group_lds(smem, g.G);
   const int tokens = g.per / a.k;  // per is a multiple of k
   const int t0 = blockIdx.x * tokens;
   const int count = min(tokens, a.T - t0);
-  choose_tokens<DT, L, V>(a, t0, count, l.sid);
+  choose_tokens<DT, L, V, NT>(a, t0, count, l.sid);
   __syncthreads();
-  if (g.blocks == 1)
+  if (NT == kThreads && g.blocks == 1)
     group_alone(g, l);
   else
-    write_counts(g, l, count * a.k);
+    write_counts<NT>(g, l, count * a.k);
 }
 
 // First launch of qw_group_rows: everything for one block, else its counts.
@@ -552,8 +732,8 @@ int topk_lanes(int E, int k) {
 // and the top-k takes few passes; else two passes of the top-k a block (16384
 // tokens of 8 in 128: 10 us, 17 with twice as many), more where there would
 // be over 256 blocks, at most kSlots. A multiple of k.
-int block_slots_of(int T, int k, int lanes) {
-  const int pass = kThreads / lanes;
+int block_slots(int T, int E, int k) {
+  const int pass = kThreads / topk_lanes(E, k);
   if (T <= 4 * pass && (long long)T * k <= kSlots) return T * k;
   long long tokens = 2 * pass;
   while (2 * tokens * k <= kSlots && T > tokens * 256) tokens *= 2;
@@ -561,7 +741,6 @@ int block_slots_of(int T, int k, int lanes) {
   return (int)(tokens * k);
 }
 
-int block_slots(int T, int E, int k) { return block_slots_of(T, k, topk_lanes(E, k)); }
 
 // Lanes a token takes in the choice by scores, and the experts that a lane
 // holds: as in the top-k, with a lane at least for every group.
@@ -570,6 +749,17 @@ int scored_lanes(int E, int k, int groups) {
   lanes = lanes < 16 ? 16 : lanes;
   while (lanes < groups) lanes *= 2;
   return lanes;
+}
+// Slots of a block: one pass of the choice a block (64 tokens, 8 of 256: two
+// launches with 4 blocks 15.7 us, one with a block of 4 passes 34), more
+// where there would be over 256 blocks, at most kSlots.
+int scored_slots(int T, int E, int k, int groups) {
+  const int pass = kThreads / scored_lanes(E, k, groups);
+  if (T <= pass) return T * k;
+  long long tokens = pass;
+  while (2 * tokens * k <= kSlots && T > tokens * 256) tokens *= 2;
+  while (tokens > 1 && tokens * k > kSlots) tokens /= 2;
+  return (int)(tokens * k);
 }
 int scored_held(int E, int groups, int lanes) {
   int per = lanes;  // lanes of a group
@@ -611,10 +801,20 @@ template <int DT>
 qw_status launch_scored(const ScoredArgs &a, const GroupArgs &g, hipStream_t s) {
   const size_t lds = group_lds_bytes(g.G);
   const int lanes = scored_lanes(a.E, a.k, a.groups), held = scored_held(a.E, a.groups, lanes);
-#define QW_SCORED(L, V)                                                            \
-  if (lanes == (L) && held == (V)) {                                               \
-    QW_HIP_TRY(launch(scored_kernel<DT, L, V>, g.blocks, kThreads, lds, s, a, g)); \
-    return launch_place(g, s);                                                     \
+  // blocks of several passes have twice the threads where their registers allow
+  // it: a pass is a chain of exchanges, which other waves fill (16384 tokens, 8
+  // of 256: 39 us, with 512 threads 46)
+  const bool twice = g.blocks > 1 && g.per / a.k > kThreads / lanes;
+#define QW_SCORED(L, V)                                                                          \
+  if (lanes == (L) && held == (V)) {                                                             \
+    if constexpr (V <= 8) {                                                                      \
+      if (twice) {                                                                               \
+        QW_HIP_TRY(launch(scored_kernel<DT, L, V, 2 * kThreads>, g.blocks, 2 * kThreads, lds, s, a, g)); \
+        return launch_place(g, s);                                                               \
+      }                                                                                          \
+    }                                                                                            \
+    QW_HIP_TRY(launch(scored_kernel<DT, L, V, kThreads>, g.blocks, kThreads, lds, s, a, g));     \
+    return launch_place(g, s);                                                                   \
   }
   QW_SCORED(16, 4)
   QW_SCORED(16, 8)
@@ -707,7 +907,7 @@ size_t qw_route_scored_workspace_bytes(int T, int E, int top_k, int n_groups) {
   if (T < 1 || E < 1 || E > QW_MAX_GROUPS || top_k < 1 || top_k > E || top_k > QW_MAX_TOPK) return 0;
   if (n_groups < 1 || n_groups > QW_MAX_EXPERT_GROUPS || E % n_groups) return 0;
   const long long n = (long long)T * top_k;
-  return n <= QW_MAX_ROWS ? qw::counts_bytes(n, qw::block_slots_of(T, top_k, qw::scored_lanes(E, top_k, n_groups)), E) : 0;
+  return n <= QW_MAX_ROWS ? qw::counts_bytes(n, qw::scored_slots(T, E, top_k, n_groups), E) : 0;
 }
 
 qw_status qw_route_scored(const void *logits, qw_dtype dtype, int T, int E, int top_k, qw_route_score score,
@@ -725,7 +925,7 @@ qw_status qw_route_scored(const void *logits, qw_dtype dtype, int T, int E, int 
   if (top_k > E / n_groups * top_groups || !(fabsf(scale) < INFINITY)) return QW_ERR_INVALID_ARG;
   const long long n = (long long)T * top_k;
   if (E > QW_MAX_GROUPS || n > QW_MAX_ROWS) return QW_ERR_UNSUPPORTED;
-  const int per = block_slots_of(T, top_k, scored_lanes(E, top_k, n_groups));
+  const int per = scored_slots(T, E, top_k, n_groups);
   const size_t need = counts_bytes(n, per, E);
   if (need && (!workspace || workspace_bytes < need)) return QW_ERR_INVALID_ARG;
   if (!aligned16(logits) || !aligned16(bias) || !aligned16(ids) || !aligned16(weights) || !aligned16(offsets) ||
