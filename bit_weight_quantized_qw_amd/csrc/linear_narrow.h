@@ -107,11 +107,14 @@ __global__ __launch_bounds__(64 * W) void narrow_kernel(LinearArgs a) {
 #pragma unroll
     for (int j = 0; j < SUB; ++j) {
       const bool in = k < K && wn[j] >= 0;
-      const uint32_t oc = in ? (uint32_t)wn[j] * (uint32_t)(K / kCodeDiv) + (uint32_t)k / kCodeDiv : kOob;
       const uint32_t os = in ? (uint32_t)wn[j] * (uint32_t)(K / kScaleDiv) + (uint32_t)k / kScaleDiv : kOob;
 #pragma unroll
       for (int i = 0; i < CH::kCodes; i += 4) {
-        const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(rc, (int)(in ? oc + 4 * i : kOob), 0, 0);
+        // the four lane groups' pieces of a column side by side: of 2-bit codes 64
+        // weights each, of 4-bit ones the group lg (then 4 + lg) of 32
+        const int kc = k2 ? k : ch * kChunk + i * 32 + lg * 32;
+        const uint32_t oc = (uint32_t)max(wn[j], 0) * (uint32_t)(K / kCodeDiv) + (uint32_t)kc / kCodeDiv;
+        const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(rc, (int)(wn[j] >= 0 && kc < K ? oc : kOob), 0, 0);
         d.c[j][i] = v[0]; d.c[j][i + 1] = v[1]; d.c[j][i + 2] = v[2]; d.c[j][i + 3] = v[3];
       }
       if (kFew && !kN) continue;  // load_few_scales
@@ -193,9 +196,9 @@ __global__ __launch_bounds__(64 * W) void narrow_kernel(LinearArgs a) {
       const u32x2 hi = *reinterpret_cast<const u32x2 *>(entry((w >> 8) & 0xFFu));
       o.b = u32x4{lo[0], lo[1], hi[0], hi[1]};
     } else if (k4) {
-      o.b = Int4<DT>::operand(c[j][(4 * h + s) % CH::kCodes], sixteen);
+      o.b = Int4<DT>::operand(c[j][(2 * s + h) % CH::kCodes], sixteen);
     } else {
-      const uint32_t w = c[j][(4 * h + s) % CH::kCodes];
+      const uint32_t w = c[j][(2 * s + h) % CH::kCodes];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const u32x2 l = *reinterpret_cast<const u32x2 *>(entry((w >> (8 * q)) & 0xFFu));
