@@ -168,8 +168,12 @@ struct XLoad {
   static constexpr int kBytes = k8 ? 1 : 2;
   static constexpr int DT = XT == QW_DT_BF16 ? QW_DT_BF16 : QW_DT_F16;
   typedef uint32_t raw __attribute__((ext_vector_type(k8 ? 2 : 4)));
-  static __device__ raw load(const void *p, size_t element) {
-    return *reinterpret_cast<const raw *>(reinterpret_cast<const char *>(p) + element * kBytes);
+  // at byte `offset` (a lane's, kOob reads zeros) + `scalar` (uniform)
+  static __device__ raw load(__amdgpu_buffer_rsrc_t r, uint32_t offset, int scalar) {
+    if constexpr (k8)
+      return __builtin_amdgcn_raw_buffer_load_b64(r, (int)offset, scalar, 0);
+    else
+      return __builtin_amdgcn_raw_buffer_load_b128(r, (int)offset, scalar, 0);
   }
   static __device__ u32x4 operand(raw r) {
     if constexpr (XT == QW_DT_E4M3) {

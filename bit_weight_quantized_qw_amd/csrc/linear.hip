@@ -139,10 +139,13 @@ Plan make_plan(const qw_weight &w, int M, bool gated, bool gemv) {
   return p;
 }
 
+// The rows of a tile lie within 32-bit offsets.
+constexpr int kMostK = 1 << 22;
+
 bool takes(const qw_weight *w, int M) {
   if (!w || M < 1 || M > QW_MAX_ROWS) return false;
   if (w->format != QW_FMT_2BIT_G32 && w->format != QW_FMT_NF4_B64 && w->format != QW_FMT_INT4_G32) return false;
-  return w->N > 0 && w->K > 0 && w->K % 64 == 0 && (unsigned long long)w->N * w->K < (1ull << 32);
+  return w->N > 0 && w->K > 0 && w->K % 64 == 0 && w->K < kMostK && (unsigned long long)w->N * w->K < (1ull << 32);
 }
 
 template <int FMT>
@@ -186,7 +189,7 @@ qw_status qgemm_linear(const qw_weight *w, const void *X, qw_dtype x_dtype, cons
   if (ep->residual == Y && ep->residual_dtype != y_dtype) return QW_ERR_INVALID_ARG;
   if (!aligned16(X) || !aligned16(x_scales) || !aligned16(Y) || !aligned16(ep->bias) || !aligned16(ep->residual))
     return QW_ERR_ALIGNMENT;
-  if (w->K % 64 || (unsigned long long)w->N * w->K >= (1ull << 32) || M > QW_MAX_ROWS) return QW_ERR_UNSUPPORTED;
+  if (!takes(w, M)) return QW_ERR_UNSUPPORTED;
   const size_t need = qw_linear_workspace_bytes(w, M);
   if (need && (!workspace || workspace_bytes < need)) return QW_ERR_INVALID_ARG;
   if (need && !aligned16(workspace)) return QW_ERR_ALIGNMENT;

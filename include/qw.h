@@ -828,8 +828,18 @@ size_t qw_linear_workspace_bytes(const qw_weight *w, int M);
  * Activations are finite (a row with an infinity or NaN gives values that are
  * not, in that row alone) and below 2^110 in size. fp32 accumulation, and
  * everything behind the sums in fp32.
- * K must be a multiple of 64 and N K below 2^32. Errors: INVALID_ARG,
- * ALIGNMENT, UNSUPPORTED (also M > QW_MAX_ROWS), HIP. */
+ * What is rounded before the product goes by the kernel, which is chosen by an
+ * estimate of its time from M, N, K and the format, so a row's last bits depend
+ * on how many rows share the call:
+ *  - one row (2-bit: up to three) of F16, not gated: the decode GEMVs, with
+ *    their roundings;
+ *  - few rows: fp32 sums of exact code levels are scaled, no weight is rounded
+ *    (an NF4 level is two numbers of 16 bits);
+ *  - more rows: the weights are rounded to 16 bits, as qgemm_prefill does (F16:
+ *    to fp16 after a power of two per column, see qgemm_experts; the other
+ *    types: to bf16, in which 8-bit activations are exact), anchors too.
+ * K must be a multiple of 64 and below 2^22, N K below 2^32. Errors:
+ * INVALID_ARG, ALIGNMENT, UNSUPPORTED (also M > QW_MAX_ROWS), HIP. */
 qw_status qgemm_linear(const qw_weight *w, const void *X, qw_dtype x_dtype,
                        const float *x_scales, int M, const qw_epilogue *ep, void *Y,
                        qw_dtype y_dtype, void *workspace, size_t workspace_bytes,

@@ -66,7 +66,13 @@ def test_linear_refusals(L):
         assert call(**kw) == ALIGN, kw
     assert call(w=weight(K=96)) == UNSUP
     assert call(w=weight(N=1 << 20, K=1 << 12)) == UNSUP
+    assert call(w=weight(N=4, K=1 << 22)) == UNSUP
     assert call(M=qw.QW_MAX_ROWS + 1) == UNSUP
+    big = weight(N=4096, K=8192)
+    need = L.qw_linear_workspace_bytes(big, 100)  # K in parts
+    assert need >= 2 * 100 * 4096 * 4 and L.qw_linear_workspace_bytes(big, 1) == 0
+    assert call(w=big, M=100, nb=need - 1) == INV and call(w=big, M=100, ws=None, nb=need) == INV
+    assert call(w=big, M=100, ws=ODD, nb=need) == ALIGN
     assert L.qw_linear_workspace_bytes(None, 4) == L.qw_linear_workspace_bytes(weight(), 0) == 0
     assert L.qw_linear_workspace_bytes(weight(K=96), 4) == L.qw_linear_workspace_bytes(weight(fmt=9), 4) == 0
 
