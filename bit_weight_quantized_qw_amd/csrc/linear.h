@@ -199,26 +199,6 @@ struct XLoad {
   }
 };
 
-// Eight e4m3 or int8 numbers as bf16 (exact: no more than 8 significant bits).
-template <int XT>
-__device__ inline u32x4 eight_as_bf16(u32x2 r) {
-  u32x4 o;
-#pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    const uint32_t w = r[q];
-    if constexpr (XT == QW_DT_E4M3) {
-      o[2 * q] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, false));
-      o[2 * q + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, true));
-    } else {
-      // the upper halves of the numbers as fp32
-      const uint32_t f0 = __builtin_bit_cast(uint32_t, (float)(int8_t)w), f1 = __builtin_bit_cast(uint32_t, (float)(int8_t)(w >> 8));
-      const uint32_t f2 = __builtin_bit_cast(uint32_t, (float)(int8_t)(w >> 16)), f3 = __builtin_bit_cast(uint32_t, (float)(int8_t)(w >> 24));
-      o[2 * q] = __builtin_amdgcn_perm(f1, f0, 0x07060302u);
-      o[2 * q + 1] = __builtin_amdgcn_perm(f3, f2, 0x07060302u);
-    }
-  }
-  return o;
-}
 // One element of activations, as 16 bits of DT.
 template <int XT, int DT>
 __device__ inline uint32_t one_as_16(const void *p, size_t element) {

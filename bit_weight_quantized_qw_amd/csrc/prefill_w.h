@@ -62,9 +62,10 @@ struct LinearTallArgs : PrefillArgs {
   static constexpr bool kMask = MASK;
   static constexpr bool kIn8 = XT == QW_DT_E4M3 || XT == QW_DT_I8;
   static constexpr int kRows = ROWS;
-  // e4m3 and int8 numbers are bf16 numbers
-  static constexpr int kType = XT == QW_DT_F16 ? QW_DT_F16 : QW_DT_BF16;
-  static __device__ u32x4 operand(u32x2 r) { return eight_as_bf16<XT>(r); }
+  // e4m3 and int8 numbers are fp16 numbers (and bf16 ones, but a weight has three
+  // bits more in fp16)
+  static constexpr int kType = XT == QW_DT_BF16 ? QW_DT_BF16 : QW_DT_F16;
+  static __device__ u32x4 operand(u32x2 r) { return XLoad<XT>::operand(r); }
   static __device__ uint32_t one(const void *p, size_t i) { return one_as_16<XT, kType>(p, i); }
   const uint32_t *mask;    // [K/32]
   int m_first;             // the launch's first row among all
@@ -438,7 +439,11 @@ __global__ __launch_bounds__(256 * WM) void prefill_w_kernel(Args a) {
       float am = __builtin_bit_cast(float, w[j][8]);
       if constexpr (kFit) am *= fit[j];
       // elements kk*16 + hk*8 .. +7 = bytes 4*(2kk+hk) .. +3 of the 32 code bytes
-      const uint32_t c = hk ? w[j][2 * kk + 1] : w[j][2 * kk];
+      uint32_t c;
+      if constexpr (Args::kLinear)  // (picked as for INT4, for the same reason)
+        c = __builtin_amdgcn_perm(w[j][2 * kk + 1], w[j][2 * kk], hk ? 0x07060504u : 0x03020100u);
+      else
+        c = hk ? w[j][2 * kk + 1] : w[j][2 * kk];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         // v_perm: byte 0 <- lane_rep (source byte 4), byte 1 <- code byte q
@@ -579,8 +584,8 @@ __global__ __launch_bounds__(256 * WM) void prefill_w_kernel(Args a) {
       for (int i = 0; i < IM; ++i)  // rows past M are not stored
         xrow[i] = reinterpret_cast<const uint16_t *>(reinterpret_cast<const char *>(a.X) + (size_t)min(m0 + xr + 32 * WM * i, a.M - 1) * K * XB);
       for (int o0 = part * BK; o0 < a.n_out; o0 += a.parts * BK) {
-        uint32_t at[8];
-        if (FMT == QW_FMT_2BIT_G32) {  // past the last: channel 0
+        if constexpr (FMT == QW_FMT_2BIT_G32) {
+          uint32_t at[8];  // past the last: channel 0
           const u32x4 lo = __builtin_amdgcn_raw_buffer_load_b128(ri, (o0 + xc) * 4, 0, 0);
           const u32x4 hi = __builtin_amdgcn_raw_buffer_load_b128(ri, (o0 + xc) * 4 + 16, 0, 0);
 #pragma unroll
@@ -588,24 +593,37 @@ __global__ __launch_bounds__(256 * WM) void prefill_w_kernel(Args a) {
             at[q] = q < 4 ? lo[q & 3] : hi[q & 3];
             if (at[q] >= (uint32_t)K) at[q] = 0;
           }
-        } else {
+          uint32_t v[IM][8];  // all of a step's elements are on their way together
 #pragma unroll
-          for (int q = 0; q < 8; ++q) at[q] = (uint32_t)min(o0 + xc + q, a.n_out - 1);
-        }
-        uint32_t v[IM][8];  // all of a step's elements are on their way together
+          for (int i = 0; i < IM; ++i)
 #pragma unroll
-        for (int i = 0; i < IM; ++i)
+            for (int q = 0; q < 8; ++q) v[i][q] = Args::one(xrow[i], at[q]);
 #pragma unroll
-          for (int q = 0; q < 8; ++q) v[i][q] = Args::one(xrow[i], at[q]);
+          for (int i = 0; i < IM; ++i) {
+            u32x4 w;
 #pragma unroll
-        for (int i = 0; i < IM; ++i) {
-          u32x4 w;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const uint32_t lo = o0 + xc + 2 * q < a.n_out ? v[i][2 * q] : 0u, hi = o0 + xc + 2 * q + 1 < a.n_out ? v[i][2 * q + 1] : 0u;
-            w[q] = lo | (hi << 16);
+            for (int q = 0; q < 4; ++q) {
+              const uint32_t a0 = o0 + xc + 2 * q < a.n_out ? v[i][2 * q] : 0u, a1 = o0 + xc + 2 * q + 1 < a.n_out ? v[i][2 * q + 1] : 0u;
+              w[q] = a0 | (a1 << 16);
+            }
+            *reinterpret_cast<u32x4 *>(xs + 32 * WM * i * LDA) = w;
           }
-          *reinterpret_cast<u32x4 *>(xs + 32 * WM * i * LDA) = w;
+        } else {  // the first channels: eight consecutive ones (K is a multiple of 64)
+#pragma unroll
+          for (int i = 0; i < IM; ++i) {
+            const xraw r = *reinterpret_cast<const xraw *>(reinterpret_cast<const char *>(xrow[i]) + (o0 + xc < K ? o0 + xc : 0) * XB);
+            u32x4 w;
+            if constexpr (Args::kIn8)
+              w = Args::operand(r);
+            else
+              w = r;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const int o = o0 + xc + 2 * q;
+              w[q] &= (o < a.n_out ? 0xFFFFu : 0u) | (o + 1 < a.n_out ? 0xFFFF0000u : 0u);
+            }
+            *reinterpret_cast<u32x4 *>(xs + 32 * WM * i * LDA) = w;
+          }
         }
         __syncthreads();
 #pragma unroll 1

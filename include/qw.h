@@ -835,9 +835,9 @@ size_t qw_linear_workspace_bytes(const qw_weight *w, int M);
  *    their roundings;
  *  - few rows: fp32 sums of exact code levels are scaled, no weight is rounded
  *    (an NF4 level is two numbers of 16 bits);
- *  - more rows: the weights are rounded to 16 bits, as qgemm_prefill does (F16:
- *    to fp16 after a power of two per column, see qgemm_experts; the other
- *    types: to bf16, in which 8-bit activations are exact), anchors too.
+ *  - more rows: the weights are rounded to 16 bits, anchors too: to bf16 for
+ *    BF16 activations, as qgemm_prefill does, else to fp16 after a power of two
+ *    per column (see qgemm_experts).
  * K must be a multiple of 64 and below 2^22, N K below 2^32. Errors:
  * INVALID_ARG, ALIGNMENT, UNSUPPORTED (also M > QW_MAX_ROWS), HIP. */
 qw_status qgemm_linear(const qw_weight *w, const void *X, qw_dtype x_dtype,

@@ -62,7 +62,7 @@ def linear64(m, x64, kind, rounded, bias=None, act=None, gated=False, residual=N
     dt = torch.bfloat16 if kind == "bf16" else torch.float16  # of the operands
     extra = half_step(dt) ** 2 if m.fmt == "nf4" else 0.0  # a level is two numbers of dt
     if rounded:
-        extra = half_step(torch.bfloat16 if kind in TOP else dt) + 2 * F32
+        extra = half_step(dt) + 2 * F32
     z = x64 @ m.W1.T
     tz = ((m.K + 64) * F32 + extra) * (np.abs(x64) @ m.mag1.T) + 2 * F32 * np.abs(z)
     if bias is not None:
