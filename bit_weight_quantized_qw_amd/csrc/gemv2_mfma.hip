@@ -1494,7 +1494,7 @@ static qw_status launch_linear_b(const ArgsLinear &a, int grid, size_t lds, hipS
 
 qw_status launch_linear(const qw_weight &w, const uint16_t *x, int M, const Finish &fin, int cus, hipStream_t s) {
   const bool i4 = w.format == QW_FMT_INT4_G32;
-  if (M < 1 || M > (i4 ? 1 : 3)) return QW_ERR_UNSUPPORTED;
+  if (M < 1 || M > (i4 ? 1 : 3) || (size_t)w.N * (w.K / (i4 ? 2 : 4)) >= kOob) return QW_ERR_UNSUPPORTED;
   ArgsLinear a{};
   int grid = 0;
   void *ys[1] = {fin.Y};

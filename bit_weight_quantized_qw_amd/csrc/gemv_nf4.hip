@@ -363,6 +363,7 @@ qw_status launch_linear_uw(const ArgsNf4Linear &a, int grid, size_t lds, hipStre
 
 qw_status launch_linear_gemv_nf4(const qw_weight &w, const uint16_t *x, const Finish &fin, int cus, hipStream_t s) {
   // one row, planned as qgemv_nf4 plans it
+  if ((size_t)w.N * (w.K / 2) >= (1ull << 31)) return QW_ERR_UNSUPPORTED;
   const int K = w.K, NH = K / 32;
   int W = 1;
   while (W < 8 && W * 64 * 4 < NH) W *= 2;

@@ -26,6 +26,44 @@ __global__ __launch_bounds__(256) void join_kernel(Finish a, int parts, int col_
   store_four(a, m, n, shape_values(a, s, up, scale_at(a, m), bias_at(a, n), bias_up_at(a, n)) + residual_at(a, m, n));
 }
 
+// Rows of bf16 as rows of fp16 times a power of two a row, for gated products by
+// tall tiles: rounded to bf16, the weights of gate and up would leave 1.7 times
+// the error that Y's own rounding leaves (2.9e-3 against 1.7e-3 of Y, 2000 rows
+// of 27648 x 5120 in INT4), rounded to fp16 they leave no more than it. A bf16
+// number is an fp16 one from the row's largest down to 2^-28 of it. Bound by
+// memory; a workgroup reads its row twice, the second time from the cache.
+__global__ __launch_bounds__(256) void to_fp16_kernel(const uint16_t *X, uint16_t *out, float *scales, int m_first, int K) {
+  __shared__ uint32_t tops[4];
+  const size_t m = (size_t)m_first + blockIdx.x;
+  const u32x4 *from = reinterpret_cast<const u32x4 *>(X + m * K);
+  uint32_t top = 0;  // the largest pattern without its sign
+  for (int i = threadIdx.x; i < K / 8; i += 256) {
+    const u32x4 v = from[i];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) top = max(top, max(v[q] & 0x7FFFu, (v[q] >> 16) & 0x7FFFu));
+  }
+#pragma unroll
+  for (int d = 32; d; d >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d, 64));
+  if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = top;
+  __syncthreads();
+  top = max(max(tops[0], tops[1]), max(tops[2], tops[3]));
+  // the largest to 2^14 .. 2^15; rows of zeros, and with an infinity or a NaN, as they are
+  const int e = (int)(top >> 7) - 127;
+  const int up = top > 0 && e < 128 ? min(14 - e, 126) : 0;
+  const float f = __builtin_bit_cast(float, (uint32_t)(127 + up) << 23);
+  if (threadIdx.x == 0) scales[m] = __builtin_bit_cast(float, (uint32_t)(127 - up) << 23);
+  u32x4 *to = reinterpret_cast<u32x4 *>(out + m * K);
+  for (int i = threadIdx.x; i < K / 8; i += 256) {
+    const u32x4 v = from[i];
+    u32x4 w;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      w[q] = Op<QW_DT_F16>::bits(__builtin_bit_cast(float, v[q] << 16) * f) |
+             (Op<QW_DT_F16>::bits(__builtin_bit_cast(float, v[q] & 0xFFFF0000u) * f) << 16);
+    to[i] = w;
+  }
+}
+
 // How a call runs: a decode GEMV, the narrow kernel with tiles of `shape`, or the
 // tall one, the first high_tiles tiles of columns with 256 rows; and the parts
 // of K.
@@ -33,7 +71,17 @@ enum class Kernel { kGemv, kNarrow, kTall };
 struct Plan {
   Kernel kernel;
   int shape, high_tiles, parts;
+  bool to_fp16;  // bf16 activations, as fp16 ones
 };
+
+// Workspace: the parts' sums, then fp16 activations and their rows' scales.
+size_t parts_bytes(const Plan &p, int M, int N) {
+  return p.parts > 1 ? ((size_t)p.parts * M * N * sizeof(float) + 15) / 16 * 16 : 0;
+}
+size_t fp16_bytes(int M, int K) { return (size_t)M * K * 2; }
+size_t workspace_of(const Plan &p, int M, int N, int K) {
+  return parts_bytes(p, M, N) + (p.to_fp16 ? fp16_bytes(M, K) + (size_t)M * sizeof(float) : 0);
+}
 
 // Tile and waves of the narrow kernel for row blocks MR (0: up to four rows): as
 // many workgroups and waves as fill the CUs, more columns a wave where there
@@ -107,9 +155,9 @@ double narrow_time(int fmt, bool anchors, int M, int N, int K, int shape) {
 }
 
 // gemv: the call is one that a decode GEMV takes (fp16 activations, not gated).
-Plan make_plan(const qw_weight &w, int M, bool gated, bool gemv) {
+Plan make_plan(const qw_weight &w, int M, bool gated, int x_dtype, bool gemv) {
   const int fmt = w.format, N = w.N, K = w.K, out_n = gated ? N / 2 : N;
-  Plan p{Kernel::kNarrow, 0, 0, 1};
+  Plan p{Kernel::kNarrow, 0, 0, 1, false};
   const int forced = tune(QW_TUNE_LINEAR_ROW_BLOCKS);
   const int most_gemv = fmt == QW_FMT_2BIT_G32 ? 3 : 1;
   const int cols = tall_columns(gated), nt = (out_n + cols - 1) / cols;
@@ -136,6 +184,7 @@ Plan make_plan(const qw_weight &w, int M, bool gated, bool gemv) {
   }
   const int parts = tune(QW_TUNE_LINEAR_PARTS), step = p.kernel == Kernel::kTall ? 64 : 256;
   if (parts > 0) p.parts = parts < K / step ? parts : K / step > 1 ? K / step : 1;
+  p.to_fp16 = p.kernel == Kernel::kTall && gated && x_dtype == QW_DT_BF16;
   return p;
 }
 
@@ -159,14 +208,9 @@ qw_status run(const LinearArgs &a, const Plan &p, hipStream_t s) {
 
 extern "C" {
 
-size_t qw_linear_workspace_bytes(const qw_weight *w, int M) {
-  if (!qw::takes(w, M)) return 0;
-  int parts = 1;  // gated or not
-  for (int gated = 0; gated < 2; ++gated) {
-    const qw::Plan p = qw::make_plan(*w, M, gated != 0, false);
-    if (p.parts > parts) parts = p.parts;
-  }
-  return parts > 1 ? (size_t)parts * (size_t)M * (size_t)w->N * sizeof(float) : 0;
+size_t qw_linear_workspace_bytes(const qw_weight *w, qw_dtype x_dtype, int M, int gated) {
+  if (!qw::takes(w, M) || (gated && w->N % 2)) return 0;
+  return qw::workspace_of(qw::make_plan(*w, M, gated != 0, x_dtype, false), M, w->N, w->K);
 }
 
 qw_status qgemm_linear(const qw_weight *w, const void *X, qw_dtype x_dtype, const float *x_scales, int M,
@@ -190,12 +234,12 @@ qw_status qgemm_linear(const qw_weight *w, const void *X, qw_dtype x_dtype, cons
   if (!aligned16(X) || !aligned16(x_scales) || !aligned16(Y) || !aligned16(ep->bias) || !aligned16(ep->residual))
     return QW_ERR_ALIGNMENT;
   if (!takes(w, M)) return QW_ERR_UNSUPPORTED;
-  const size_t need = qw_linear_workspace_bytes(w, M);
+  const size_t need = qw_linear_workspace_bytes(w, x_dtype, M, ep->gated);
   if (need && (!workspace || workspace_bytes < need)) return QW_ERR_INVALID_ARG;
   if (need && !aligned16(workspace)) return QW_ERR_ALIGNMENT;
   int cus = 0;
   QW_TRY(current_device(&cus));
-  Plan plan = make_plan(*w, M, ep->gated != 0, x_dtype == QW_DT_F16 && !ep->gated);
+  Plan plan = make_plan(*w, M, ep->gated != 0, x_dtype, x_dtype == QW_DT_F16 && !ep->gated);
   LinearArgs a{};
   a.X = X;
   a.codes = w->codes;
@@ -221,7 +265,20 @@ qw_status qgemm_linear(const qw_weight *w, const void *X, qw_dtype x_dtype, cons
     const qw_status st = w->format == QW_FMT_NF4_B64 ? launch_linear_gemv_nf4(*w, x, a.fin, cus, s)
                                                      : gemv2m::launch_linear(*w, x, M, a.fin, cus, s);
     if (st != QW_ERR_UNSUPPORTED) return st;
-    plan = make_plan(*w, M, gated, false);
+    plan = make_plan(*w, M, gated, x_dtype, false);
+  }
+  if (plan.to_fp16) {
+    char *const at = reinterpret_cast<char *>(workspace) + parts_bytes(plan, M, w->N);
+    float *const scales = reinterpret_cast<float *>(at + fp16_bytes(M, w->K));
+    const int most = (int)kMostBlocks;
+    for (int m = 0; m < M; m += most) {
+      const int now = M - m < most ? M - m : most;
+      QW_HIP_TRY(launch(to_fp16_kernel, (unsigned)now, 256, 0, s, reinterpret_cast<const uint16_t *>(X), reinterpret_cast<uint16_t *>(at),
+                        scales, m, w->K));
+    }
+    a.X = at;
+    a.x_dtype = QW_DT_F16;
+    a.fin.x_scales = scales;
   }
   if (w->format == QW_FMT_2BIT_G32)
     QW_TRY(run<QW_FMT_2BIT_G32>(a, plan, s));

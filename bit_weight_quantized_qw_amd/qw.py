@@ -178,7 +178,7 @@ def lib():
         "qw_route_scored": (c_i, [c_p, c_i, c_i, c_i, c_i, c_i, c_p, c_i, c_i, c_i, c_i, ctypes.c_float, c_p, c_p, c_p,
                                   c_p, c_p, c_sz, c_p]),
         "qw_rmsnorm": (c_i, [c_p, c_i, c_p, c_i, c_p, c_i, ctypes.c_float, c_i, c_i, c_p, c_p, c_p, c_i, c_p, c_p]),
-        "qw_linear_workspace_bytes": (c_sz, [W, c_i]),
+        "qw_linear_workspace_bytes": (c_sz, [W, c_i, c_i, c_i]),
         "qgemm_linear": (c_i, [W, c_p, c_i, c_p, c_i, ctypes.POINTER(qw_epilogue), c_p, c_i, c_p, c_sz, c_p]),
         "qw_tune_set": (c_i, [c_i, c_i]),
         "qw_tune_get": (c_i, [c_i]),
@@ -1155,9 +1155,10 @@ def qw_rmsnorm(x, weight, eps=1e-6, residual=None, residual_out=None, perm=None,
 _ACTS = {None: QW_ACT_NONE, "relu": QW_ACT_RELU, "silu": QW_ACT_SILU, "gelu": QW_ACT_GELU, "gelu_tanh": QW_ACT_GELU_TANH}
 
 
-def qw_linear_workspace_bytes(pw, M):
+def qw_linear_workspace_bytes(pw, x_dtype, M, gated=False):
+    """Workspace bytes of qgemm_linear for M rows of the torch type x_dtype."""
     v = pw.view()
-    return int(lib().qw_linear_workspace_bytes(ctypes.byref(v), int(M)))
+    return int(lib().qw_linear_workspace_bytes(ctypes.byref(v), _act_dtypes()[x_dtype], int(M), 1 if gated else 0))
 
 
 def qgemm_linear(pw, X, bias=None, act=None, gated=False, residual=None, x_scales=None, out_dtype=None, out=None,
@@ -1206,7 +1207,7 @@ def qgemm_linear(pw, X, bias=None, act=None, gated=False, residual=None, x_scale
         ep.residual = residual.data_ptr()
         used.append(residual)
     v = pw.view()
-    nb = int(lib().qw_linear_workspace_bytes(ctypes.byref(v), M))
+    nb = int(lib().qw_linear_workspace_bytes(ctypes.byref(v), x_dt, M, ep.gated))
     ws = _workspace(workspace, nb, X.device) if nb else None
     if ws is not None:
         used.append(ws)

@@ -802,10 +802,11 @@ typedef struct {
   int32_t gated;          /* 0, or 1: w is a merged gate/up weight */
 } qw_epilogue;
 
-/* Device workspace bytes of qgemm_linear for M rows (0 when none is needed or
- * an argument is out of range): fp32 partial sums where K is cut into parts.
+/* Device workspace bytes of qgemm_linear for M rows of x_dtype, gated or not (0
+ * when none is needed or an argument is out of range): fp32 partial sums where
+ * K is cut into parts, fp16 activations where gated bf16 ones take tall tiles.
  * Host only. */
-size_t qw_linear_workspace_bytes(const qw_weight *w, int M);
+size_t qw_linear_workspace_bytes(const qw_weight *w, qw_dtype x_dtype, int M, int gated);
 
 /* The product of any number of rows with one packed matrix, and what a layer
  * does behind it, in one pass:
@@ -822,7 +823,8 @@ size_t qw_linear_workspace_bytes(const qw_weight *w, int M);
  *            ep->residual may be Y (added in place) where the types agree;
  *            no other input may overlap Y.
  *   workspace device scratch of workspace_bytes >=
- *            qw_linear_workspace_bytes(w, M) (may be NULL when that is 0);
+ *            qw_linear_workspace_bytes(w, x_dtype, M, ep->gated) (may be NULL
+ *            when that is 0);
  *            its contents on entry do not matter. Calls that overlap in time,
  *            replays of captured ones among them, must not share it.
  * Activations are finite (a row with an infinity or NaN gives values that are
@@ -836,8 +838,10 @@ size_t qw_linear_workspace_bytes(const qw_weight *w, int M);
  *  - few rows: fp32 sums of exact code levels are scaled, no weight is rounded
  *    (an NF4 level is two numbers of 16 bits);
  *  - more rows: the weights are rounded to 16 bits, anchors too: to bf16 for
- *    BF16 activations, as qgemm_prefill does, else to fp16 after a power of two
- *    per column (see qgemm_experts).
+ *    BF16 activations that are not gated, as qgemm_prefill does, else to fp16
+ *    after a power of two per column (see qgemm_experts); gated BF16 activations
+ *    become fp16 after one per row, which keeps those above 2^-28 of the row's
+ *    largest.
  * K must be a multiple of 64 and below 2^22, N K below 2^32. Errors:
  * INVALID_ARG, ALIGNMENT, UNSUPPORTED (also M > QW_MAX_ROWS), HIP. */
 qw_status qgemm_linear(const qw_weight *w, const void *X, qw_dtype x_dtype,

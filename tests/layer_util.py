@@ -61,10 +61,16 @@ def linear64(m, x64, kind, rounded, bias=None, act=None, gated=False, residual=N
     import torch
     dt = torch.bfloat16 if kind == "bf16" else torch.float16  # of the operands
     extra = half_step(dt) ** 2 if m.fmt == "nf4" else 0.0  # a level is two numbers of dt
+    small = 0.0
+    if rounded and gated and kind == "bf16":
+        # fp16 operands: what lies below 2^-28 of a row's largest is off by at most
+        # 2^-39 of it (half of fp16's smallest step, 2^-25, where the largest is 2^14)
+        dt = torch.float16
+        small = 2.0 ** -39 * np.abs(x64).max(1, keepdims=True) * np.abs(m.W1).sum(1)[None]
     if rounded:
         extra = half_step(dt) + 2 * F32
     z = x64 @ m.W1.T
-    tz = ((m.K + 64) * F32 + extra) * (np.abs(x64) @ m.mag1.T) + 2 * F32 * np.abs(z)
+    tz = ((m.K + 64) * F32 + extra) * (np.abs(x64) @ m.mag1.T) + 2 * F32 * np.abs(z) + small
     if bias is not None:
         z = z + bias
         tz = tz + 2 * F32 * np.abs(z)

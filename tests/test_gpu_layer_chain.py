@@ -170,7 +170,7 @@ def test_given_workspaces(tune):
     layer = Layer(32)
     tune(qw.QW_TUNE_LINEAR_PARTS, 2)
     x, _ = start(100, 9)
-    nb = qw.qw_linear_workspace_bytes(layer.o.pw, 100)
+    nb = qw.qw_linear_workspace_bytes(layer.o.pw, x.dtype, 100)
     assert nb == 2 * 100 * H * 4
     want = qw.qgemm_linear(layer.o.pw, x)
     ws = torch.full((nb + 64,), 255, dtype=torch.uint8, device="cuda")

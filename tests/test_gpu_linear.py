@@ -140,6 +140,25 @@ def test_fp16_weights_of_any_size_keep_their_bits(tune):
             assert_close(got, want, tol + extra * (np.abs(x64) @ m.mag1.T), torch.float32, f"{fmt} {size}")
 
 
+def test_gated_bf16_rows_of_any_size(tune):
+    """Tall gated tiles: rows of 1e-30, 1e30, zeros and one with an infinity, one large channel."""
+    import torch
+    tune(qw.QW_TUNE_LINEAR_ROW_BLOCKS, 8)
+    m = Matrix("int4", 128, 256, 5, 50)
+    X, _, _ = activations(40, 256, "bf16", 51)
+    X[0] *= 1e-30
+    X[1] *= 1e8
+    X[2] = 0
+    X[3, 7] = float("inf")
+    X[4, 9] = 3e4
+    x64 = X.double().cpu().numpy()
+    y = qw.qgemm_linear(m.pw, X, gated=True, out_dtype=torch.float32)
+    keep = [i for i in range(40) if i != 3]
+    want, tol = linear64(m, x64[keep], "bf16", True, gated=True)
+    assert_close(y[keep], want, tol, torch.float32)
+    assert bool((y[2] == 0).all()) and not bool(torch.isfinite(y[3]).any())
+
+
 def test_rows_do_not_depend_on_each_other_and_ends_stay():
     """A row's values do not change with its place; nothing is written behind Y."""
     import torch

@@ -69,12 +69,14 @@ def test_linear_refusals(L):
     assert call(w=weight(N=4, K=1 << 22)) == UNSUP
     assert call(M=qw.QW_MAX_ROWS + 1) == UNSUP
     big = weight(N=4096, K=8192)
-    need = L.qw_linear_workspace_bytes(big, 100)  # K in parts
-    assert need >= 2 * 100 * 4096 * 4 and L.qw_linear_workspace_bytes(big, 1) == 0
+    need = L.qw_linear_workspace_bytes(big, F16, 100, 0)  # K in parts
+    assert need >= 2 * 100 * 4096 * 4 and L.qw_linear_workspace_bytes(big, F16, 1, 0) == 0
+    assert L.qw_linear_workspace_bytes(big, BF16, 3000, 1) >= 3000 * 8192 * 2  # the activations in fp16
     assert call(w=big, M=100, nb=need - 1) == INV and call(w=big, M=100, ws=None, nb=need) == INV
     assert call(w=big, M=100, ws=ODD, nb=need) == ALIGN
-    assert L.qw_linear_workspace_bytes(None, 4) == L.qw_linear_workspace_bytes(weight(), 0) == 0
-    assert L.qw_linear_workspace_bytes(weight(K=96), 4) == L.qw_linear_workspace_bytes(weight(fmt=9), 4) == 0
+    size = L.qw_linear_workspace_bytes
+    assert size(None, F16, 4, 0) == size(weight(), F16, 0, 0) == size(weight(N=17), BF16, 4000, 1) == 0
+    assert size(weight(K=96), F16, 4, 0) == size(weight(fmt=9), F16, 4, 0) == 0
 
 
 def test_route_scored_refusals(L):
