@@ -47,9 +47,10 @@ __global__ __launch_bounds__(256) void to_fp16_kernel(const uint16_t *X, uint16_
   if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = top;
   __syncthreads();
   top = max(max(tops[0], tops[1]), max(tops[2], tops[3]));
-  // the largest to 2^14 .. 2^15; rows of zeros, and with an infinity or a NaN, as they are
-  const int e = (int)(top >> 7) - 127;
-  const int up = top > 0 && e < 128 ? min(14 - e, 126) : 0;
+  // the largest to 2^14 .. 2^15 (beside an infinity or a NaN as beside the largest
+  // number, so that no finite one becomes infinite), rows of zeros as they are
+  const int e = min((int)(top >> 7) - 127, 127);
+  const int up = top > 0 ? min(14 - e, 126) : 0;
   const float f = __builtin_bit_cast(float, (uint32_t)(127 + up) << 23);
   if (threadIdx.x == 0) scales[m] = __builtin_bit_cast(float, (uint32_t)(127 - up) << 23);
   u32x4 *to = reinterpret_cast<u32x4 *>(out + m * K);
@@ -85,7 +86,11 @@ size_t workspace_of(const Plan &p, int M, int N, int K) {
 
 // Tile and waves of the narrow kernel for row blocks MR (0: up to four rows): as
 // many workgroups and waves as fill the CUs, more columns a wave where there
-// are enough of them (what a wave loads of X serves them all).
+// are enough of them (what a wave loads of X serves them all). With tiles of 32
+// and 64 columns, 8 waves each, us: 16 rows of 5120 x 5120 in 2-bit 16.9 / 21.9,
+// of 11008 x 4096 in NF4 19.1 / 16.4, of 27648 x 5120 in INT4 44.8 / 35.7. Tiles
+// of four rows against sixteen, one row of 8192 x 28672: 2-bit 39 / 47, NF4 33 /
+// 36, INT4 37 / 36 (so it has none).
 int pick_narrow(int MR, int fmt, int out_n, int K, bool gated) {
   const int blocks = (out_n + 15) / 16 * (gated ? 2 : 1), chunks = (K + 255) / 256;
   if (MR == 0) {
@@ -159,7 +164,14 @@ Plan make_plan(const qw_weight &w, int M, bool gated, int x_dtype, bool gemv) {
   const int fmt = w.format, N = w.N, K = w.K, out_n = gated ? N / 2 : N;
   Plan p{Kernel::kNarrow, 0, 0, 1, false};
   const int forced = tune(QW_TUNE_LINEAR_ROW_BLOCKS);
-  const int most_gemv = fmt == QW_FMT_2BIT_G32 ? 3 : 1;
+  // Rows that a decode GEMV takes, if it can keep K whole (else its sums would go
+  // through memory; up to four rows take the narrow kernel then). GEMV / narrow, us:
+  //   2-bit, anchors   5120 x 5120, 1..3 rows   7.6/10.5  9.5/10.8  11.7/11.1
+  //                   27648 x 5120            15.0/25.4 19.4/26.6  24.0/27.4
+  //   2-bit            5120 x 5120             6.3/7.8   8.5/8.4   10.4/8.9
+  //                    8192 x 8192             8.7/12.3 12.1/13.0  15.0/13.3
+  //   NF4, 1 row 5120 x 5120 6.8/9.4;  INT4, anchors 8.5/10.4
+  const int most_gemv = fmt == QW_FMT_2BIT_G32 ? (w.n_out > 0 ? 3 : 2) : 1;
   const int cols = tall_columns(gated), nt = (out_n + cols - 1) / cols;
   if (gemv && M <= most_gemv && forced <= 0) p.kernel = Kernel::kGemv;
   const int MR = forced > 0 && forced < 8 ? (forced == 4 ? 0 : forced) : M <= 4 ? 0 : M <= 16 ? 1 : 2;
@@ -176,7 +188,7 @@ Plan make_plan(const qw_weight &w, int M, bool gated, int x_dtype, bool gemv) {
       p.high_tiles = high_tiles;
       p.parts = parts;
     };
-    for (int parts = 1; parts <= 16 && K / 64 / parts >= 2; parts *= 2) {
+    for (int parts = 1; parts <= 16 && (parts == 1 || K / 64 / parts >= 2); parts *= 2) {
       consider(tall_time(fmt, w.n_out > 0, M, nt, N, K, false, parts), 0, parts);
       consider(tall_time(fmt, w.n_out > 0, M, nt, N, K, true, parts), nt, parts);
     }

@@ -6,8 +6,8 @@
 // the group's scale multiplies the fp32 sum, so no weight is rounded (an NF4
 // level is two 16-bit numbers).
 //
-// Tile: 16 MR rows times 64 columns, by four waves that each take a part of K;
-// their sums meet in LDS in wave order.
+// Tile: 4 or 16 MR rows times 16 SUB columns, by W waves that each take a part
+// of K; their sums meet in LDS in wave order.
 #pragma once
 
 #include "linear.h"

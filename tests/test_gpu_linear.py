@@ -159,6 +159,34 @@ def test_gated_bf16_rows_of_any_size(tune):
     assert bool((y[2] == 0).all()) and not bool(torch.isfinite(y[3]).any())
 
 
+def test_gated_bf16_infinity_beside_large_numbers(tune):
+    """Tall gated tiles: one infinity among numbers past fp16's range gives infinities of
+    the weights' signs, not NaN."""
+    import torch
+    tune(qw.QW_TUNE_LINEAR_ROW_BLOCKS, 8)
+    m = Matrix("nf4", 128, 256, 0, 52)
+    X = torch.full((40, 256), 1e6, dtype=torch.bfloat16, device="cuda")
+    X[3, 7] = float("inf")
+    y = qw.qgemm_linear(m.pw, X, gated=True, out_dtype=torch.float32)[3].cpu().numpy()
+    sign = np.sign(m.W1[:64, 7]) * np.sign(m.W1[64:, 7])  # no weight: infinity times 0
+    assert (sign != 0).sum() > 30
+    assert (y[sign != 0] == np.inf * sign[sign != 0]).all() and np.isnan(y[sign == 0]).all()
+
+
+@pytest.mark.parametrize("fmt", ["2bit", "nf4", "int4"])
+@pytest.mark.parametrize("gated", [False, True])
+def test_one_step_of_K_and_more_rows_than_a_launch_of_narrow_tiles(fmt, gated):
+    """K of 64 by 2^20 + 3 rows and 17000 columns, 70 million waves of narrow tiles: the rows at both ends."""
+    import torch
+    M, N = (1 << 20) + 3, 17000
+    m = Matrix(fmt, N, 64, 0, 53)
+    X = torch.randn(M, 64, device="cuda").half()
+    y = qw.qgemm_linear(m.pw, X, gated=gated, out_dtype=torch.float16)
+    for rows in (slice(0, 40), slice(M - 40, M)):
+        want, tol = linear64(m, X[rows].double().cpu().numpy(), "f16", True, gated=gated)
+        assert_close(y[rows], want, tol, torch.float16)
+
+
 def test_rows_do_not_depend_on_each_other_and_ends_stay():
     """A row's values do not change with its place; nothing is written behind Y."""
     import torch
