@@ -833,8 +833,8 @@ size_t qw_linear_workspace_bytes(const qw_weight *w, qw_dtype x_dtype, int M, in
  * What is rounded before the product goes by the kernel, which is chosen by an
  * estimate of its time from M, N, K and the format, so a row's last bits depend
  * on how many rows share the call:
- *  - one row (2-bit: up to three) of F16, not gated: the decode GEMVs, with
- *    their roundings;
+ *  - one row (2-bit: two, with anchors three) of F16, not gated, where K is short
+ *    enough to stay whole: the decode GEMVs, with their roundings;
  *  - few rows: fp32 sums of exact code levels are scaled, no weight is rounded
  *    (an NF4 level is two numbers of 16 bits);
  *  - more rows: the weights are rounded to 16 bits, anchors too: to bf16 for
