@@ -1,6 +1,6 @@
-// The products of qgemm_linear by narrow tiles, for few rows. What bounds them: the packed weights' stream,
-// read once; so the kernel is built to keep loads of codes in flight and to
-// decode a weight in about one instruction. The scheme is the one of the
+// The products of qgemm_linear by narrow tiles, for few rows. What should bound
+// them is the packed weights' stream, read once; so the kernel is built to keep
+// loads of codes in flight and to decode a weight in about one instruction. The scheme is the one of the
 // experts' narrow tiles: a matrix instruction of 16 x 16 x 32 covers the 32
 // weights of one scale group, the products are with the bare code levels and
 // the group's scale multiplies the fp32 sum, so no weight is rounded (an NF4
@@ -8,6 +8,11 @@
 //
 // Tile: 4 or 16 MR rows times 16 SUB columns, by W waves that each take a part
 // of K; their sums meet in LDS in wave order.
+//
+// Measured, 7 rows of 8192 x 28672: INT4 with anchors and e4m3 rows 42 us (3.2
+// TB/s), NF4 41, 2-bit with anchors 59; one row in NF4 33. What bounds them: the
+// loads' address units, busy 0.60 of the cycles in the first of these (a load
+// touches 16 rows), beside 0.38 of vector issue and 0.09 of matrix products.
 #pragma once
 
 #include "linear.h"

@@ -14,9 +14,9 @@
 // pass and one exchange: the scale of a row is the largest y over the largest
 // number of the type, and y is h weight times one factor a row.
 //
-// Measured: 8192 x 8192 in bf16 with the residual, y in bf16 98 us (5.4 TB/s; a
-// copy of 1 GiB here 5.2), in e4m3 93; 8192 x 1024 13.2 us (5.1 TB/s); 777 x
-// 5120 with an fp32 residual 11.2 us, in a permuted order 13.8 (the gather from
+// Measured: 8192 x 8192 in bf16 with the residual, y in bf16 97 us (5.5 TB/s; a
+// copy of 1 GiB here 5.2), in e4m3 91; 8192 x 1024 12.8 us (5.2 TB/s); 777 x
+// 5120 with an fp32 residual 11.2 us, in a permuted order 13.5 (the gather from
 // LDS); one row of 5120 4.2 us. Rows that do not start on 16 bytes (K not a
 // multiple of 8) go by single elements: 4096 x 5119 68 us, 2.5 TB/s.
 #include <math.h>
