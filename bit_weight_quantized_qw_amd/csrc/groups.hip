@@ -364,7 +364,8 @@ __device__ inline bool choose32(const ScoredArgs &a, const TokenLanes<L, V> &t, 
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const float s = a.score == QW_ROUTE_SOFTMAX ? c[v] * inv : __frcp_rn(1.0f + __expf(-x[v]));
-      c[v] = x[v] > -INFINITY ? s + bias[v] : -INFINITY;
+      const float choice = s + bias[v];
+      c[v] = x[v] > -INFINITY && choice > -INFINITY ? choice : -INFINITY;  // NaN is taken as -inf
     }
   }
   if (a.top_groups < a.groups) {
