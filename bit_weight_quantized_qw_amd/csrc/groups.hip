@@ -192,7 +192,7 @@ __device__ inline void topk_tokens(const RouteArgs &a, int t0, int count, int32_
 // fp32 agree in fp32 as soon as they come near 1, and a bias of 0.1 leaves
 // scores of 1e-4 three digits. So the choice is made in fp32 first, and where
 // two values that it depends on are nearer to each other than fp32 can tell
-// (kUnsure), it is made again in 64 bits: some tokens in a hundred with fp32
+// (unsure), it is made again in 64 bits: some tokens in a hundred with fp32
 // logits, all with equal choices. Without a bias a score's order is its logit's,
 // and only sums of two are ever unsure. 16384 tokens, 8 of 256 in 4 of 8 groups:
 // 39 us, all of it in 64 bits 52.
@@ -324,13 +324,20 @@ __device__ inline int choose64(const ScoredArgs &a, const TokenLanes<L, V> &t, c
   return id;
 }
 
-// How near two fp32 choices may lie and still be unsure. A sigmoid is off by
-// |l| s (1 - s) 2^-23 + s (1 - s) 2^-23 (the exponential's argument, rounded
-// twice, and its step) and two roundings of numbers up to 1: less than 3e-7. A
-// softmax's sum adds up to 16 roundings of itself: less than 1.2e-6. The bias's
-// addition rounds once more, and two values are compared.
-__device__ inline float unsure(const ScoredArgs &a, float c) {
-  return (a.score == QW_ROUTE_SIGMOID ? 8e-7f : 3e-6f) + 0x1p-22f * fabsf(c);
+// How near two fp32 choices may lie and still be unsure: more than both are off by
+// together (two groups' sums: than half of it, so each group brings one).
+// A sigmoid is off by |l| s (1 - s) 2^-23 + s (1 - s) 2^-23 (the exponential's
+// argument, rounded twice, and its step) and two roundings of numbers up to 1: less
+// than 3e-7. Softmax scores share the error of their sum, V - 1 + log2 L half steps.
+// Their exponentials, 2.5 d + 2 half steps each at a distance of d from the largest,
+// weigh in by their scores, which are 1 together at most: 11 half steps for two
+// scores and their sum, 14 for four; the quotient and the product round once each.
+// A choice is rounded once more behind the bias, a sum of two twice: `size` is what
+// the terms add up to without their signs (terms that cancel keep their errors).
+template <int L, int V>
+__device__ inline float unsure(const ScoredArgs &a, float size) {
+  constexpr int kLog = L == 16 ? 4 : L == 32 ? 5 : 6;
+  return (a.score == QW_ROUTE_SIGMOID ? 8e-7f : (float)(V - 1 + kLog + 16) * 0x1p-24f) + 0x1p-22f * size;
 }
 
 // The same with 32-bit keys; chosen[j] (LDS) receives choice j. Returns whether
@@ -381,10 +388,11 @@ __device__ inline bool choose32(const ScoredArgs &a, const TokenLanes<L, V> &t, 
       one = fmaxf(one, f);
     }
     const float value = sums && two > -INFINITY ? one + two : one;
-    const float near = scores ? 2.0f * unsure(a, value) : -1.0f;
+    const float mine = unsure<L, V>(a, fabsf(one) + (sums && two > -INFINITY ? fabsf(two) : 0.0f));
     int before = 0;
     for (int g = 0; g < a.groups; ++g) {
       const float o = __shfl(value, g * t.P, L);
+      const float near = !scores ? -1.0f : mine + (a.bias ? __shfl(mine, g * t.P, L) : mine);
       before += o > value || (o == value && g < t.group);
       // (a group that has no expert left is behind all others in any case)
       if (g != t.group && value > -INFINITY && o > -INFINITY && !(fabsf(o - value) > near)) sure = false;
@@ -417,7 +425,7 @@ __device__ inline bool choose32(const ScoredArgs &a, const TokenLanes<L, V> &t, 
     best = lanes_max<L>(best);
     if (a.bias && best) {
       const float value = from_ordered32(best);
-      if (!(last - value > unsure(a, value))) sure = false;  // j = 0: infinity, and NaN where the value is infinite too
+      if (!(last - value > unsure<L, V>(a, fabsf(value)))) sure = false;  // j = 0: infinity, and NaN where the value is infinite too
       last = value;
     }
     if (j == a.k || __all(best == 0)) break;

@@ -27,3 +27,24 @@ def test_bias_of_nan(score, dtype, E, n, top, k):
     bias[: (n - top) * size] = np.nan
     bias[(n - top) * size + size // 2] = np.inf
     run(logits(9, E, 70), dtype, k, score, bias, n, top, "top2")
+
+
+@pytest.mark.parametrize("size", [1.0, 100.0, 1e3, 1e5])
+@pytest.mark.parametrize("by", ["max", "top2"])
+def test_biases_that_cancel(size, by):
+    """Groups of two whose biases add up to nothing: a group's value is a small sum
+    of large numbers."""
+    rng = np.random.default_rng(int(size))
+    bias = (size * rng.uniform(0.5, 1, (8, 1)) * [1, -1]).astype(np.float32).reshape(-1)
+    run(logits(4000, 16, 71), "f32", 4, "sigmoid", bias, 8, 4, by)
+    run(logits(4000, 16, 72), "f32", 4, "softmax", bias, 8, 4, by)
+
+
+def test_a_large_bias_in_one_group():
+    """One expert kept out by -1e9, one in by 1e6: the other groups' order is
+    theirs."""
+    bias = (0.1 * np.random.default_rng(8).standard_normal(64)).astype(np.float32)
+    bias[3], bias[17] = -1e9, 1e6
+    for n, top in ((8, 3), (32, 9), (1, 1)):
+        for score in ("sigmoid", "softmax"):
+            run(logits(3000, 64, 73), "f32", 6, score, bias, n, top, "top2")
