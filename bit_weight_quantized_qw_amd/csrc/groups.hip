@@ -194,7 +194,9 @@ __device__ inline void topk_tokens(const RouteArgs &a, int t0, int count, int32_
 // two values that it depends on are nearer to each other than fp32 can tell
 // (unsure), it is made again in 64 bits: some tokens in a hundred with fp32
 // logits, all with equal choices. Without a bias a score's order is its logit's,
-// and only sums of two are ever unsure. 16384 tokens, 8 of 256 in 4 of 8 groups:
+// and only sums of two are unsure, and logits whose scores may be one 64-bit number
+// (may_level). A token's choice is that of its own 64-bit scores, whichever path
+// its wave takes. 16384 tokens, 8 of 256 in 4 of 8 groups:
 // 39 us, all of it in 64 bits 52.
 //
 // The chosen experts' scores are computed again from their logits, one a lane
@@ -340,6 +342,16 @@ __device__ inline float unsure(const ScoredArgs &a, float size) {
   return (a.score == QW_ROUTE_SIGMOID ? 8e-7f : (float)(V - 1 + kLog + 16) * 0x1p-24f) + 0x1p-22f * size;
 }
 
+// Without a bias the logits have the order of the scores, but the scores' 64-bit
+// numbers may be equal where the logits are not, and then the lower expert comes
+// first: sigmoids above 37 are all 1, what lies below -745 (softmax: that far below
+// the largest) is 0, and logits next to 0 have one score. Whether a logit may be one
+// of those, with room. A pair of others has two numbers: sigmoids of fp32 logits up
+// to 20 are 4e-15 apart, logits of 2^-12 and more 2^-36.
+__device__ inline bool may_level(const ScoredArgs &a, float l, float most) {
+  return (a.score == QW_ROUTE_SIGMOID ? l > 20.0f || l < -700.0f : l - most < -700.0f) || fabsf(l) < 0x1p-12f;
+}
+
 // The same with 32-bit keys; chosen[j] (LDS) receives choice j. Returns whether
 // it is the choice in 64 bits for sure.
 //
@@ -396,6 +408,11 @@ __device__ inline bool choose32(const ScoredArgs &a, const TokenLanes<L, V> &t, 
       before += o > value || (o == value && g < t.group);
       // (a group that has no expert left is behind all others in any case)
       if (g != t.group && value > -INFINITY && o > -INFINITY && !(fabsf(o - value) > near)) sure = false;
+    }
+    const bool level = !scores && value > -INFINITY && may_level(a, value, most);
+    if (__any(level)) {
+      for (int g = 0; g < a.groups; ++g)
+        if (__shfl((int)level, g * t.P, L) && level && g != t.group) sure = false;
     }
     if (before >= a.top_groups) {
 #pragma unroll
@@ -484,17 +501,30 @@ __device__ inline void choose_tokens(const ScoredArgs &a, int t0, int count, int
       for (int d = L / 2; d; d >>= 1) most = fmaxf(most, __shfl_xor(most, d, L));
     }
     int32_t *const chosen = sid + i * a.k;
-    const bool sure = choose32<DT, L>(a, lanes, x, bias, most, chosen) && !(softmax && most == INFINITY);  // such a row has no scores
+    bool sure = choose32<DT, L>(a, lanes, x, bias, most, chosen) && !(softmax && most == INFINITY);  // such a row has no scores
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
     __builtin_amdgcn_wave_barrier();
     int id = sub < a.k ? chosen[sub] : -1;
-    if (__any(!sure)) {
-      id = choose64<L>(a, lanes, x, bias, most);
-      if (sub < a.k) chosen[sub] = id;
+    float l = id >= 0 ? logit_at<DT>(a.logits, (size_t)t * a.E + id) : 0.0f;
+    if (!a.bias) {  // a choice and the next, or the last and the first that is none, may have one score
+      const int lane = threadIdx.x & 63;
+      const bool level = id >= 0 && may_level(a, l, most);
+      const unsigned long long others = __ballot(id >= 0 && !level);
+      if (level && (sub == a.k - 1 || !((others >> ((lane + 1) & 63)) & 1))) sure = false;
+    }
+    const unsigned long long doubts = __ballot(!sure);
+    if (doubts) {  // of one of the wave's tokens: the others keep their choice
+      const int id64 = choose64<L>(a, lanes, x, bias, most);
+      constexpr unsigned long long kToken = L == 64 ? ~0ull : (1ull << (L % 64)) - 1;
+      if ((doubts >> ((threadIdx.x & 63) / L * L)) & kToken) {
+        id = id64;
+        if (sub < a.k) chosen[sub] = id;
+        l = id >= 0 ? logit_at<DT>(a.logits, (size_t)t * a.E + id) : 0.0f;
+      }
     }
     // normalised weights do not need the sum over all experts
     const double sum = softmax && !a.normalize ? sum64<L>(x, most) : 1.0;
-    const double w = id >= 0 ? score64(a, logit_at<DT>(a.logits, (size_t)t * a.E + id), most, sum) : 0.0;
+    const double w = id >= 0 ? score64(a, l, most, sum) : 0.0;
     double factor = (double)a.scale;
     if (a.normalize) {
       const double total = sum_of<L>(w);

@@ -621,9 +621,10 @@ size_t qw_route_scored_workspace_bytes(int T, int E, int top_k, int n_groups);
  *           (without the bias), divided by the sum of the chosen ones' scores
  *           when normalize != 0 (0 where that sum is 0); 0 where the id is -1.
  *   offsets, rows, workspace: as qw_route_topk.
- * Scores, choices and group values are computed and compared in 64 bits, so
- * the order of experts is that of the formula but for differences of some
- * 1e-15. Errors: INVALID_ARG (also top_k > E / n_groups * top_groups),
+ * Experts and groups are ordered as their scores, choices and values compare in
+ * 64 bits, so by the formula but for differences of some 1e-15 (sigmoids of
+ * logits above 37 are all 1, and equal). A token's outputs do not depend on the
+ * other tokens. Errors: INVALID_ARG (also top_k > E / n_groups * top_groups),
  * ALIGNMENT, UNSUPPORTED (E > QW_MAX_GROUPS, T * top_k > QW_MAX_ROWS), HIP. */
 qw_status qw_route_scored(const void *logits, qw_dtype dtype, int T, int E, int top_k,
                           qw_route_score score, const float *bias, int n_groups, int top_groups,

@@ -5,6 +5,9 @@ test_gpu_route_scored."""
 import numpy as np
 import pytest
 
+from bit_weight_quantized_qw_amd import qw
+from gpu_util import to_dev
+from routed_util import tdt
 from test_gpu_route_scored import logits, run
 
 pytestmark = pytest.mark.gpu
@@ -48,3 +51,37 @@ def test_a_large_bias_in_one_group():
     for n, top in ((8, 3), (32, 9), (1, 1)):
         for score in ("sigmoid", "softmax"):
             run(logits(3000, 64, 73), "f32", 6, score, bias, n, top, "top2")
+
+
+# logits whose 64-bit scores are one number (1 above 37.5, 0 below -745 or that
+# far below the largest, 1/2 next to 0), beside others
+SAME = {"sigmoid": [38, 40, 45, 100, 3e4], "softmax": [-1e4, -1.5e4, -2e4, -3e4]}
+LOW = [-768, -800, -896, -6e4]
+TINY = [1e-30, 0.0, -1e-25, 3e-28, 1e-38]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("n,top", [(1, 1), (8, 3)])
+@pytest.mark.parametrize("by", ["max", "top2"])
+def test_a_token_does_not_depend_on_its_neighbours(score, dtype, n, top, by):
+    """Tokens with scores that are equal in 64 bits though the logits are not, in
+    every order, beside tokens that tie and ordinary ones: the formula's choice,
+    and alone the same as among others."""
+    import torch
+    rng = np.random.default_rng(9)
+    E, k, T = 64, 6, 96
+    x = logits(T, E, 74)
+    x[1::4] = np.round(x[1::4])  # ties
+    for t in range(0, T, 4):
+        if t % 8 == 0:
+            x[t] = rng.choice(SAME[score] + ([] if t % 16 else [5.0]), E)
+        else:
+            x[t] = rng.choice(TINY + ([0.0] if t % 16 == 4 else [-3.0]), E)
+        x[t + 2] = rng.choice(LOW if score == "sigmoid" else LOW + [0.0], E)
+        x[t + 3, rng.choice(E, 10)] = rng.choice(SAME[score], 10)
+    r = run(x, dtype, k, score, None, n, top, by)
+    X = to_dev(x.astype(np.float32)).to(tdt(dtype))
+    for t in range(T):
+        one = qw.qw_route_scored(X[t:t + 1].contiguous(), k, score=score, n_groups=n, top_groups=top, group_by=by)
+        assert torch.equal(one.ids[0], r.ids[t]) and torch.equal(one.weights[0], r.weights[t]), t
