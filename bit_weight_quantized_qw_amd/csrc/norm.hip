@@ -92,16 +92,20 @@ __device__ inline void store_values(void *p, size_t i, const float (&v)[V], int 
   }
 }
 
-// The same in 8 bits; the values are within the type's range but for a
-// rounding of the scale's inverse.
+// V values as bytes of an 8-bit type; they are within its range but for a rounding
+// of the scale's inverse.
 template <int V>
-__device__ inline void store_8bit(void *p, size_t i, const float (&v)[V], int dt) {
-  uint32_t w[V == 8 ? 2 : 1] = {0};
+struct Bytes {
+  uint32_t w[V == 8 ? 2 : 1];
+};
+template <int V>
+__device__ inline Bytes<V> to_8bit(const float (&v)[V], int dt) {
+  Bytes<V> b = {};
   if (dt == QW_DT_I8) {
 #pragma unroll
     for (int q = 0; q < V; ++q) {
       const int n = (int)rintf(__builtin_amdgcn_fmed3f(v[q], -127.0f, 127.0f));
-      w[q / 4] |= ((uint32_t)n & 0xFFu) << (8 * (q & 3));
+      b.w[q / 4] |= ((uint32_t)n & 0xFFu) << (8 * (q & 3));
     }
   } else {
     float c[V];
@@ -110,18 +114,22 @@ __device__ inline void store_8bit(void *p, size_t i, const float (&v)[V], int dt
     if constexpr (V == 8) {
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
-        w[q] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c[4 * q], c[4 * q + 1], 0, false);
-        w[q] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c[4 * q + 2], c[4 * q + 3], (int)w[q], true);
+        b.w[q] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c[4 * q], c[4 * q + 1], 0, false);
+        b.w[q] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c[4 * q + 2], c[4 * q + 3], (int)b.w[q], true);
       }
     } else {
-      w[0] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c[0], 0.0f, 0, false);
+      b.w[0] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c[0], 0.0f, 0, false);
     }
   }
+  return b;
+}
+template <int V>
+__device__ inline void store_bytes(void *p, size_t i, const Bytes<V> &b) {
   uint8_t *o = reinterpret_cast<uint8_t *>(p) + i;
   if constexpr (V == 8)
-    *reinterpret_cast<u32x2 *>(o) = u32x2{w[0], w[1]};
+    *reinterpret_cast<u32x2 *>(o) = u32x2{b.w[0], b.w[1]};
   else
-    o[0] = (uint8_t)w[0];
+    o[0] = (uint8_t)b.w[0];
 }
 
 // The smallest scale of a row: its inverse is finite, and rows of zeros (or of
@@ -131,12 +139,13 @@ constexpr float kLeastScale = 0x1p-100f;
 // XS, RS: bytes of an element of x and of the residual (0: none); W: waves of
 // a row; IT: runs of V elements that a lane holds, at most. V is 8, or 1
 // where rows do not start on 16 bytes.
-// MORE: 8 bits or a permuted order.
-template <int XS, int RS, int W, int IT, int V, bool MORE>
+// IN8: y in 8 bits; PERM: in a permuted order.
+template <int XS, int RS, int W, int IT, int V, bool IN8, bool PERM>
 __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void norm_kernel(NormArgs a) {
   constexpr int kRows = W == 1 ? 4 : 1;  // rows of a workgroup
   constexpr int kLanes = 64 * W;         // lanes of a row
-  extern __shared__ float smem[];        // [kRows][K] with perm
+  // with perm, the row in its own order: h weight in fp32, or 8-bit elements
+  extern __shared__ __attribute__((aligned(16))) float smem[];  // [kRows][K] of either
   __shared__ double sums[W];
   __shared__ uint32_t tops[W];
   const int row_of = W == 1 ? (int)threadIdx.x >> 6 : 0;
@@ -158,7 +167,6 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void norm_kernel(NormArgs a)
       if (k < K) load_raw(rv[i], a.residual, row + k);
     if (k < K && !w32) load_raw(gv[i], a.weight, k);
   }
-  const bool in8 = MORE && (a.y_dtype == QW_DT_E4M3 || a.y_dtype == QW_DT_I8);
   // the weights of run i: in registers, or 32-bit ones read again
   auto weights = [&](int i, int k, float (&g)[V]) {
     if (w32) {
@@ -187,13 +195,12 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void norm_kernel(NormArgs a)
     if (RS != 0 && a.h_out) store_values<V>(a.h_out, row + k, h[i], a.r_dtype);
     float g[V];
     weights(i, k, g);
-    if constexpr (MORE) {
+    if constexpr (IN8) {
 #pragma unroll
-      for (int q = 0; q < V; ++q) {
-        const float p = h[i][q] * g[q];
-        if (a.perm) smem[(size_t)row_of * K + k + q] = p;
-        top = max(top, __builtin_bit_cast(uint32_t, p) & 0x7FFFFFFFu);
-      }
+      for (int q = 0; q < V; ++q) top = max(top, __builtin_bit_cast(uint32_t, h[i][q] * g[q]) & 0x7FFFFFFFu);
+    } else if constexpr (PERM) {
+#pragma unroll
+      for (int q = 0; q < V; ++q) smem[(size_t)row_of * K + k + q] = h[i][q] * g[q];
     } else {
 #pragma unroll
       for (int q = 0; q < V; ++q) h[i][q] *= g[q];
@@ -206,15 +213,25 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void norm_kernel(NormArgs a)
 #pragma unroll
   for (int d = 32; d; d >>= 1) {
     sum += __shfl_xor(sum, d, 64);
-    if constexpr (MORE) top = max(top, (uint32_t)__shfl_xor((int)top, d, 64));
+    if constexpr (IN8) top = max(top, (uint32_t)__shfl_xor((int)top, d, 64));
   }
+  // the row's LDS is written before any of it is read
+  auto row_written = [&]() {
+    if constexpr (W > 1) {
+      __syncthreads();
+    } else {  // by one wave
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+      __builtin_amdgcn_wave_barrier();
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+    }
+  };
   if constexpr (W > 1) {
     const int wv = threadIdx.x >> 6;
     if ((threadIdx.x & 63) == 0) {
       sums[wv] = sum;
       tops[wv] = top;
     }
-    __syncthreads();
+    row_written();
     sum = 0.0;
 #pragma unroll
     for (int w = 0; w < W; ++w) {
@@ -222,15 +239,12 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void norm_kernel(NormArgs a)
       top = max(top, tops[w]);
     }
   } else {
-    // the row's LDS is written and read by one wave
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+    row_written();
   }
   const double inv = 1.0 / sqrt(sum / (double)K + (double)a.eps);
   float f = (float)inv;
   float f_rest = 0.0f;  // what f's rounding left
-  if (in8) {
+  if constexpr (IN8) {
     const double most = a.y_dtype == QW_DT_I8 ? 127.0 : 448.0;
     const double largest = (double)__builtin_bit_cast(float, top) * inv;
     // a row with an infinity or a NaN has no scale
@@ -241,47 +255,62 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void norm_kernel(NormArgs a)
     f = (float)factor;
     f_rest = (float)(factor - (double)f);
   }
+  uint8_t *const bytes = reinterpret_cast<uint8_t *>(smem) + (size_t)row_of * K;
 #pragma unroll
   for (int i = 0; i < IT; ++i) {
     const int k = (i * kLanes + at) * V;
     if (k >= K) continue;
     float v[V];
-    if (MORE && a.perm) {
-      Raw<4, V> from;
-      load_raw(from, a.perm, k);
-#pragma unroll
-      for (int q = 0; q < V; ++q) v[q] = from.w[q] < (uint32_t)K ? smem[(size_t)row_of * K + from.w[q]] * f : 0.0f;
-    } else if constexpr (MORE) {
+    if constexpr (IN8) {
       float g[V];
       weights(i, k, g);
 #pragma unroll
       for (int q = 0; q < V; ++q) {
         const float p = h[i][q] * g[q];
         // rounded once, so that only values next to a border of the grid could
-        // fall on its other side
-        v[q] = __builtin_fmaf(p, f, __builtin_fmaf(p, f_rest, __builtin_fmaf(h[i][q], g[q], -p) * f));
+        // fall on its other side; infinity times zero is not zero
+        v[q] = f == 0.0f ? 0.0f : __builtin_fmaf(p, f, __builtin_fmaf(p, f_rest, __builtin_fmaf(h[i][q], g[q], -p) * f));
       }
+      const Bytes<V> b = to_8bit<V>(v, a.y_dtype);
+      if constexpr (PERM)
+        store_bytes<V>(bytes, k, b);
+      else
+        store_bytes<V>(a.y, row + k, b);
     } else {
+      if constexpr (PERM) {
+        Raw<4, V> from;
+        load_raw(from, a.perm, k);
 #pragma unroll
-      for (int q = 0; q < V; ++q) v[q] = h[i][q] * f;
-    }
-    if (in8) {
-      if (f == 0.0f) {  // infinity times zero is not zero
+        for (int q = 0; q < V; ++q) v[q] = from.w[q] < (uint32_t)K ? smem[(size_t)row_of * K + from.w[q]] * f : 0.0f;
+      } else {
 #pragma unroll
-        for (int q = 0; q < V; ++q) v[q] = 0.0f;
+        for (int q = 0; q < V; ++q) v[q] = h[i][q] * f;
       }
-      store_8bit<V>(a.y, row + k, v, a.y_dtype);
-    } else {
       store_values<V>(a.y, row + k, v, a.y_dtype);
+    }
+  }
+  if constexpr (IN8 && PERM) {  // elements take the other order as they are
+    row_written();
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+      const int k = (i * kLanes + at) * V;
+      if (k >= K) continue;
+      Raw<4, V> from;
+      load_raw(from, a.perm, k);
+      Bytes<V> b = {};
+#pragma unroll
+      for (int q = 0; q < V; ++q)
+        if (from.w[q] < (uint32_t)K) b.w[q / 4] |= (uint32_t)bytes[from.w[q]] << (8 * (q & 3));
+      store_bytes<V>(a.y, row + k, b);
     }
   }
 }
 
-template <int XS, int RS, int W, int IT, int V, bool MORE>
-qw_status launch_more(const NormArgs &a, hipStream_t s) {
-  constexpr auto kernel = norm_kernel<XS, RS, W, IT, V, MORE>;
+template <int XS, int RS, int W, int IT, int V, bool IN8, bool PERM>
+qw_status launch_form(const NormArgs &a, hipStream_t s) {
+  constexpr auto kernel = norm_kernel<XS, RS, W, IT, V, IN8, PERM>;
   constexpr int kRows = W == 1 ? 4 : 1;
-  const size_t lds = a.perm ? (size_t)kRows * a.K * sizeof(float) : 0;
+  const size_t lds = PERM ? (size_t)kRows * a.K * (IN8 ? 1 : sizeof(float)) : 0;
   if (lds > 32768)
     QW_HIP_TRY(hipFuncSetAttribute(reinterpret_cast<const void *>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds));
   QW_HIP_TRY(launch(kernel, (unsigned)((a.M + kRows - 1) / kRows), W == 1 ? 256 : 64 * W, lds, s, a));
@@ -290,8 +319,9 @@ qw_status launch_more(const NormArgs &a, hipStream_t s) {
 
 template <int XS, int RS, int W, int IT, int V>
 qw_status launch_one(const NormArgs &a, hipStream_t s) {
-  const bool more = a.perm || a.y_dtype == QW_DT_E4M3 || a.y_dtype == QW_DT_I8;
-  return more ? launch_more<XS, RS, W, IT, V, true>(a, s) : launch_more<XS, RS, W, IT, V, false>(a, s);
+  if (a.y_dtype == QW_DT_E4M3 || a.y_dtype == QW_DT_I8)
+    return a.perm ? launch_form<XS, RS, W, IT, V, true, true>(a, s) : launch_form<XS, RS, W, IT, V, true, false>(a, s);
+  return a.perm ? launch_form<XS, RS, W, IT, V, false, true>(a, s) : launch_form<XS, RS, W, IT, V, false, false>(a, s);
 }
 
 template <int XS, int RS>

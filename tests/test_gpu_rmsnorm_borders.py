@@ -1,0 +1,49 @@
+"""qw_rmsnorm at the borders of the 8-bit grids and of its sizes.
+
+Bound of an 8-bit element: a lane adds at most 32 squares in fp32 (each of a sum
+rounded once: (32 + 2) 2^-24 of their sum at most, half of that in the root) and
+everything behind that is in 64 bits but h's own rounding and three of the
+element: less than 24 2^-24 of the element beside the half step of its grid."""
+
+import numpy as np
+import pytest
+
+from bit_weight_quantized_qw_amd import qw
+from layer_util import TOP, xdt
+from routed_util import F32
+from test_gpu_rmsnorm import formula, inputs
+
+pytestmark = pytest.mark.gpu
+
+
+def nearest(n, want, kind, rel=24 * F32):
+    """The elements of n are the nearest to want over their row's scale."""
+    s = n.scales.double().cpu().numpy()
+    v = n.y.double().cpu().numpy() if kind == "i8" else n.y.float().double().cpu().numpy()
+    q = want / s[:, None]
+    half = 0.5 if kind == "i8" else np.maximum(2.0 ** -4 * np.abs(q), 2.0 ** -10)
+    bad = ~(np.abs(v - q) <= half + rel * np.abs(q))
+    assert not bad.any(), (bad.sum(), np.argwhere(bad)[:3], v[bad][:3], q[bad][:3])
+    assert np.abs(v).max() <= TOP[kind]
+
+
+@pytest.mark.parametrize("y", ["e4m3", "i8"])
+@pytest.mark.parametrize("K", [1, 7, 64, 511, 520, 2048, 2056, 5120, 8191, 8192, 16384, 20001, 32768])
+def test_permuted_8_bit_rows_are_the_plain_ones(K, y):
+    """With perm, scales and elements are those without it, bit for bit, in the
+    other order; entries out of range give zeros. Both are the nearest."""
+    import torch
+    M = 100
+    X, R, W, P = inputs(M, K, "bf16", "f32", K + 1, "f32")
+    plain = qw.qw_rmsnorm(X.cuda(), W.cuda(), residual=R.cuda(), out_dtype=xdt(y))
+    bad = P.clone()
+    if K > 8:
+        bad[5], bad[6] = -1, K
+    n = qw.qw_rmsnorm(X.cuda(), W.cuda(), residual=R.cuda(), perm=bad.cuda(), out_dtype=xdt(y))
+    assert torch.equal(n.scales, plain.scales)
+    want = plain.y.view(torch.uint8)[:, P.cuda().long()]
+    if K > 8:
+        want[:, 5:7] = 0
+    got = n.y.view(torch.uint8)
+    assert torch.equal(got, want), f"{int((got != want).sum())} of {got.numel()}"
+    nearest(plain, formula(X, R, W, 1e-6)[1], y)
