@@ -251,7 +251,16 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void norm_kernel(NormArgs a)
     const bool fine = largest < (double)INFINITY;
     const float scale = fine ? fmaxf((float)(largest / most), kLeastScale) : NAN;
     if (at == 0) a.y_scales[m] = scale;
-    const double factor = fine ? inv / (double)scale : 0.0;
+    double factor = fine ? inv / (double)scale : 0.0;
+    // tiny rows by tiny weights (eps as small, or the least scale): the factor may lie
+    // past fp32's range, so h takes a part of it (h weight is below 2^-91 then)
+    if (factor > 0x1p100) {
+      factor *= 0x1p-64;
+#pragma unroll
+      for (int i = 0; i < IT; ++i)
+#pragma unroll
+        for (int q = 0; q < V; ++q) h[i][q] *= 0x1p64f;
+    }
     f = (float)factor;
     f_rest = (float)(factor - (double)f);
   }

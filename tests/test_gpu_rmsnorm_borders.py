@@ -47,3 +47,22 @@ def test_permuted_8_bit_rows_are_the_plain_ones(K, y):
     got = n.y.view(torch.uint8)
     assert torch.equal(got, want), f"{int((got != want).sum())} of {got.numel()}"
     nearest(plain, formula(X, R, W, 1e-6)[1], y)
+
+
+@pytest.mark.parametrize("perm", [False, True])
+@pytest.mark.parametrize("y", ["e4m3", "i8"])
+def test_8_bit_rows_of_tiny_numbers(y, perm):
+    """eps = 0 and rows of 1e-10 by weights of 1e-27 (a row's factor is past fp32's
+    largest number) and of zeros (the least scale, and zeros)."""
+    import torch
+    K = 640
+    X, _, _, P = inputs(5, K, "f32", None, 11)
+    X = X * 1e-10
+    for w in (1e-27, 0.0):
+        W = torch.full((K,), w)
+        n = qw.qw_rmsnorm(X.cuda(), W.cuda(), 0.0, perm=P.cuda() if perm else None, out_dtype=xdt(y))
+        want = formula(X, None, W, 0.0)[1]
+        if w:
+            nearest(n, want[:, P.numpy()] if perm else want, y)
+        else:
+            assert bool((n.scales == 2.0 ** -100).all()) and bool((n.y.view(torch.uint8) & 0x7F == 0).all())
