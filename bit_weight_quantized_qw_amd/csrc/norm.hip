@@ -33,6 +33,7 @@ struct NormArgs {
   float *y_scales;
   float eps;
   int M, K;
+  int first;  // the launch's first row
   int x_dtype, r_dtype, w_dtype, y_dtype;
 };
 
@@ -149,7 +150,7 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void norm_kernel(NormArgs a)
   __shared__ double sums[W];
   __shared__ uint32_t tops[W];
   const int row_of = W == 1 ? (int)threadIdx.x >> 6 : 0;
-  const int m = (int)blockIdx.x * kRows + row_of;
+  const int m = a.first + (int)blockIdx.x * kRows + row_of;
   if (m >= a.M) return;  // W == 1: whole waves, and no barrier below
   const int at = W == 1 ? (int)threadIdx.x & 63 : (int)threadIdx.x;
   const int K = a.K;
@@ -316,13 +317,17 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void norm_kernel(NormArgs a)
 }
 
 template <int XS, int RS, int W, int IT, int V, bool IN8, bool PERM>
-qw_status launch_form(const NormArgs &a, hipStream_t s) {
+qw_status launch_form(NormArgs a, hipStream_t s) {
   constexpr auto kernel = norm_kernel<XS, RS, W, IT, V, IN8, PERM>;
-  constexpr int kRows = W == 1 ? 4 : 1;
+  constexpr int kRows = W == 1 ? 4 : 1, kThreads = W == 1 ? 256 : 64 * W;
   const size_t lds = PERM ? (size_t)kRows * a.K * (IN8 ? 1 : sizeof(float)) : 0;
   if (lds > 32768)
     QW_HIP_TRY(hipFuncSetAttribute(reinterpret_cast<const void *>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds));
-  QW_HIP_TRY(launch(kernel, (unsigned)((a.M + kRows - 1) / kRows), W == 1 ? 256 : 64 * W, lds, s, a));
+  constexpr int kMost = (int)(0xFFFFFFFFll / kThreads) * kRows;  // a launch counts its threads in 32 bits
+  for (; a.first < a.M; a.first += kMost) {
+    const int rows = a.M - a.first < kMost ? a.M - a.first : kMost;
+    QW_HIP_TRY(launch(kernel, (unsigned)((rows + kRows - 1) / kRows), kThreads, lds, s, a));
+  }
   return QW_OK;
 }
 
@@ -376,6 +381,6 @@ extern "C" qw_status qw_rmsnorm(const void *x, qw_dtype x_dtype, const void *res
     return QW_ERR_ALIGNMENT;
   if (K > QW_MAX_NORM_K || M > QW_MAX_ROWS) return QW_ERR_UNSUPPORTED;
   QW_TRY(current_device(nullptr));
-  const NormArgs a{x, residual, weight, perm, residual_out, y, y_scales, eps, M, K, x_dtype, residual_dtype, weight_dtype, y_dtype};
+  const NormArgs a{x, residual, weight, perm, residual_out, y, y_scales, eps, M, K, 0, x_dtype, residual_dtype, weight_dtype, y_dtype};
   return x_dtype == QW_DT_F32 ? launch_residual<4>(a, as_stream(stream)) : launch_residual<2>(a, as_stream(stream));
 }

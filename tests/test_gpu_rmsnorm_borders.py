@@ -66,3 +66,21 @@ def test_8_bit_rows_of_tiny_numbers(y, perm):
             nearest(n, want[:, P.numpy()] if perm else want, y)
         else:
             assert bool((n.scales == 2.0 ** -100).all()) and bool((n.y.view(torch.uint8) & 0x7F == 0).all())
+
+
+def test_as_many_rows_as_a_call_takes():
+    """2^24 rows of 513: 2^32 threads, more than one launch may have."""
+    import torch
+    M, K = qw.QW_MAX_ROWS, 513
+    row = torch.randn(K, device="cuda").half()
+    x = row.expand(M, K).contiguous()
+    ends = torch.randn(2, 40, K, device="cuda").half()
+    x[:40], x[-40:] = ends[0], ends[1]
+    w = torch.randn(K, device="cuda").half()
+    y = qw.qw_rmsnorm(x, w, out=x).y
+    one = qw.qw_rmsnorm(row[None], w).y
+    assert torch.equal(y[:40], qw.qw_rmsnorm(ends[0], w).y) and torch.equal(y[-40:], qw.qw_rmsnorm(ends[1], w).y)
+    for at in range(40, M - 40, 1 << 20):
+        assert torch.equal(y[at:at + 1], one), at
+    at = (1 << 24) - (1 << 19)
+    assert bool((y[at:-40] == one).all())
