@@ -153,10 +153,28 @@ double tall_time(int fmt, bool anchors, int M, int nt, int N, int K, bool high, 
   const double rounds = high ? ceil(groups / 256) : groups <= 256 ? 1.0 : 1.7 * fmax(1.0, groups / 512 + 0.2);
   return 10 + steps * kStep[f][high] * rounds + (parts > 1 ? 4 + 8.0 * parts * M * N / 5.2e6 : 0);
 }
+// A narrow grid of 256 workgroups and fewer is one round, whatever its rows: each
+// of them passes through all of K. us, measured / estimated, narrow, and by 128 rows
+// with K in 16 parts (bf16 rows, anchors with INT4):
+//   2-bit           40 x 500 x  4096   16/17     16/18
+//   2-bit           40 x 500 x  8192   25/25     19/22
+//   2-bit          100 x 500 x 28672   70/68     38/42
+//   NF4             40 x 500 x 11008   32/33     40/35
+//   NF4             40 x 500 x 28672   75/74     67/67
+//   INT4            40 x 500 x  4096   18/18     18/19
+//   INT4            40 x 500 x  8192   27/28     23/24
+//   INT4           100 x 500 x 28672   78/77     49/50
+// 2-bit with anchors, bf16 rows and int8 rows, narrow, and in 16 parts: 4096 20 21,
+// 20 23; 6144 25 25, 22 27; 8192 35 34, 24 30; 28672 106 96, 46 71 (40 rows of 500).
+// A round takes 3.4e-3 a step of K there, and 2.4e-3 are counted: int8 rows take
+// longer by tall tiles than is estimated, and between the two kinds' borders (5000
+// and 7000) it is the narrow kernel that rounds no weight.
 double narrow_time(int fmt, bool anchors, int M, int N, int K, int shape) {
+  const int f = fmt == QW_FMT_2BIT_G32 ? anchors : fmt == QW_FMT_NF4_B64 ? 2 : 3;
+  constexpr double kRound[4] = {2.1e-3, 2.4e-3, 2.3e-3, 2.4e-3};
   const double macs = (double)((M + 31) / 32 * 32) * N * K;
   const bool two = shape / 100 % 100 == 2 && K < 8192;  // 16-column blocks of a wave
-  return 8 + macs / (fmt == QW_FMT_2BIT_G32 && anchors ? (two ? 45e6 : 75e6) : two ? 80e6 : 100e6);
+  return 8 + fmax(K * kRound[f], macs / (f == 1 ? (two ? 45e6 : 75e6) : two ? 80e6 : 100e6));
 }
 
 // gemv: the call is one that a decode GEMV takes (fp16 activations, not gated).
