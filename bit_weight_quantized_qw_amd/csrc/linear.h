@@ -202,14 +202,12 @@ struct XLoad {
 // One element of activations, as 16 bits of DT.
 template <int XT, int DT>
 __device__ inline uint32_t one_as_16(const void *p, size_t element) {
+  static_assert(DT == XLoad<XT>::DT, "the operands' type");
   if constexpr (XT == QW_DT_I8) {
     return Op<DT>::bits((float)reinterpret_cast<const int8_t *>(p)[element]);
   } else if constexpr (XT == QW_DT_E4M3) {
     const uint32_t b = reinterpret_cast<const uint8_t *>(p)[element];
-    if constexpr (DT == QW_DT_BF16)
-      return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.0f, false)) & 0xFFFFu;
-    else
-      return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 1.0f, false)) & 0xFFFFu;
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 1.0f, false)) & 0xFFFFu;
   } else {
     return reinterpret_cast<const uint16_t *>(p)[element];
   }

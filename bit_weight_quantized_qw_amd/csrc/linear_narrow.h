@@ -73,7 +73,8 @@ __global__ __launch_bounds__(64 * W) void narrow_kernel(LinearArgs a) {
   constexpr bool kFew = MR == 0;
   constexpr int R = kFew ? 1 : MR;        // 16-row blocks of operands
   constexpr int kHigh = kFew ? 4 : 16 * MR;
-  constexpr int kRuns = MR <= 2 ? 4 : 2;  // runs of 64 elements of X that are on their way
+  constexpr int kRuns = 4;  // runs of 64 elements of X that are on their way
+  static_assert(!kFew || !k4, "INT4 takes tiles of 16 rows");
   constexpr int kSums = W * 16 * (kCols + 4) * 4, kTable = k4 ? 0 : 256 * kEntry;
   __shared__ __attribute__((aligned(16))) char tab[kTable > kSums ? kTable : kSums];
   float(*const part)[16][kCols + 4] = reinterpret_cast<float(*)[16][kCols + 4]>(tab);
@@ -219,22 +220,16 @@ __global__ __launch_bounds__(64 * W) void narrow_kernel(LinearArgs a) {
     return o;
   };
 
-  // scale words of a few rows: those of groups lg and 4 + lg of the chunk
+  // 2-bit scale words of a few rows: those of groups lg and 4 + lg of the chunk
   auto load_few_scales = [&](int ch, CH &d) {
-    if (!kFew || kN) return;
-    constexpr uint32_t kWord = k2 ? 4 : 2;
+    if (!kFew || !k2) return;
     const int g = ch * (kChunk / 32) + lg;
 #pragma unroll
     for (int j = 0; j < SUB; ++j) {
-      const uint32_t at = (uint32_t)max(wn[j], 0) * (uint32_t)(K / kScaleDiv) + (uint32_t)g * kWord;
-      const uint32_t o0 = wn[j] >= 0 && g < K / 32 ? at : kOob, o1 = wn[j] >= 0 && g + 4 < K / 32 ? at + 4 * kWord : kOob;
-      if (k2) {
-        d.s[j][0] = __builtin_amdgcn_raw_buffer_load_b32(rs, (int)o0, 0, 0);
-        d.s[j][CH::kScales - 1] = __builtin_amdgcn_raw_buffer_load_b32(rs, (int)o1, 0, 0);
-      } else {
-        d.s[j][0] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(rs, (int)o0, 0, 0) |
-                    (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(rs, (int)o1, 0, 0) << 16;
-      }
+      const uint32_t at = (uint32_t)max(wn[j], 0) * (uint32_t)(K / kScaleDiv) + (uint32_t)g * 4;
+      const uint32_t o0 = wn[j] >= 0 && g < K / 32 ? at : kOob, o1 = wn[j] >= 0 && g + 4 < K / 32 ? at + 16 : kOob;
+      d.s[j][0] = __builtin_amdgcn_raw_buffer_load_b32(rs, (int)o0, 0, 0);
+      d.s[j][CH::kScales - 1] = __builtin_amdgcn_raw_buffer_load_b32(rs, (int)o1, 0, 0);
     }
   };
   CH next;
@@ -330,7 +325,6 @@ __global__ __launch_bounds__(64 * W) void narrow_kernel(LinearArgs a) {
       for (int q = 0; q < 2; ++q) {
         xo[q] = XL::operand(xr.v[q][0]);
         if (k2 && ANCH) xo[q] = without_anchors(xo[q], xr.drop[q]);
-        if (k4) xo[q] = Int4<DT>::order(xo[q]);
       }
 #pragma unroll
       for (int j = 0; j < SUB; ++j) {
@@ -350,9 +344,8 @@ __global__ __launch_bounds__(64 * W) void narrow_kernel(LinearArgs a) {
             u32x4 A = xo[kN ? h : q];
 #pragma unroll
             for (int t = 0; t < 4; ++t) A[t] = slot == s ? A[t] : 0u;
-            constexpr uint32_t m24 = Int4<DT>::kMinus24;
-            const uint32_t ones = k4 ? m24 : O::bits(100.0f) * 0x10001u;
-            if (!kN) sums = O::mma(A, u32x4{ones, ones, ones, ones}, sums);
+            const uint32_t hundred = O::bits(100.0f) * 0x10001u;
+            if (k2) sums = O::mma(A, u32x4{hundred, hundred, hundred, hundred}, sums);
             // step (32 weights) 4 q + s of the chunk; NF4: 2 s + h
             const int step = kN ? 2 * s + h : 4 * q + s;
 #pragma unroll
@@ -365,8 +358,7 @@ __global__ __launch_bounds__(64 * W) void narrow_kernel(LinearArgs a) {
         }
 #pragma unroll
         for (int j = 0; j < SUB; ++j) {
-          if (k4) D[j] += sums;
-          const uint32_t sw = k4 ? d.s[j][0] >> (16 * q) : d.s[j][q % CH::kScales];
+          const uint32_t sw = d.s[j][q % CH::kScales];
           const float S = kN ? __builtin_bit_cast(float, sw) : f16_bits_to_f32((uint16_t)sw);
           const float Z = f16_bits_to_f32((uint16_t)(sw >> 16));
 #pragma unroll
@@ -478,6 +470,7 @@ __global__ __launch_bounds__(64 * W) void narrow_kernel(LinearArgs a) {
 
 template <int FMT, int XT, bool ANCH, int MR, int SUB, int W>
 qw_status launch_one(LinearArgs a, hipStream_t s) {
+  if (SUB == 1 && a.fin.gated) return QW_ERR_UNSUPPORTED;  // such a tile has no up columns
   const int cols = a.fin.gated ? 8 * SUB : 16 * SUB;
   a.col_tiles = (a.fin.out_n + cols - 1) / cols;
   constexpr int kHigh = MR == 0 ? 4 : 16 * MR;
@@ -500,9 +493,7 @@ qw_status launch_shape(const LinearArgs &a, int shape, hipStream_t s) {
     QW_SHAPE(0, 2, 8)
     QW_SHAPE(0, 2, 16)
   }
-  QW_SHAPE(1, 1, 8)
   QW_SHAPE(1, 2, 8)
-  QW_SHAPE(1, 2, 16)
   QW_SHAPE(1, 4, 4)
   QW_SHAPE(1, 4, 8)
   QW_SHAPE(2, 2, 8)
