@@ -12,14 +12,17 @@
 //
 // The row's sum of squares and (8 bits) the largest |h weight| come from one
 // pass and one exchange: the scale of a row is the largest y over the largest
-// number of the type, and y is h weight times one factor a row.
+// number of the type, and y is h weight times one factor a row. With perm, LDS
+// turns the row: h weight in fp32, or the 8-bit elements as they are.
 //
-// Measured: 8192 x 8192 in bf16 with the residual, y in bf16 97 us (5.5 TB/s; a
-// copy of 1 GiB here 5.2), in e4m3 91; 8192 x 1024 12.8 us (5.2 TB/s); 777 x
-// 5120 with an fp32 residual 11.2 us, in a permuted order 13.5 (the gather from
-// LDS); one row of 5120 4.2 us. Rows that do not start on 16 bytes (K not a
-// multiple of 8) go by single elements: 4096 x 5119 68 us, 2.5 TB/s.
+// Measured: 8192 x 8192 in bf16 with the residual, y in bf16 96 us (5.6 TB/s; a
+// copy of 1 GiB here 5.2), in e4m3 89, permuted 102 (8 K single bytes a row from
+// LDS); 8192 x 1024 11.6 us (5.8 TB/s); 777 x 5120 with an fp32 residual 10.2 us, in
+// a permuted order 11.8; one row of 5120 4.2 us. Rows that do not start on 16 bytes
+// (K not a multiple of 8) go by single elements: 4096 x 5119 70 us, 2.4 TB/s.
 #include <math.h>
+
+#include <type_traits>
 
 #include "op16.h"
 
@@ -36,10 +39,6 @@ struct NormArgs {
   int first;  // the launch's first row
   int x_dtype, r_dtype, w_dtype, y_dtype;
 };
-
-__device__ inline float value16(uint32_t b, int dt) {
-  return dt == QW_DT_F16 ? Op<QW_DT_F16>::value(b & 0xFFFFu) : Op<QW_DT_BF16>::value(b & 0xFFFFu);
-}
 
 // V elements as they lie in memory, S bytes each.
 template <int S, int V>
@@ -63,12 +62,34 @@ __device__ inline void load_raw(Raw<S, V> &d, const void *p, size_t i) {
   }
 }
 
+// Their numbers (of eight, dt is asked for once).
 template <int S, int V>
-__device__ inline float raw_value(const Raw<S, V> &d, int q, int dt) {
-  if constexpr (S == 4) return __builtin_bit_cast(float, d.w[q]);
-  return value16(d.w[q / 2] >> (16 * (q & 1)), dt);
+__device__ inline void raw_values(const Raw<S, V> &d, float (&v)[V], int dt) {
+  if constexpr (S == 4) {
+#pragma unroll
+    for (int q = 0; q < V; ++q) v[q] = __builtin_bit_cast(float, d.w[q]);
+  } else if constexpr (V == 1) {
+    // both, and one of them by a mask (4096 x 5119 70 us, with a branch for each 73)
+    uint32_t f16 = dt == QW_DT_F16 ? ~0u : 0u;
+    asm("" : "+v"(f16));
+    v[0] = __builtin_bit_cast(float, (__builtin_bit_cast(uint32_t, Op<QW_DT_F16>::value(d.w[0] & 0xFFFFu)) & f16) |
+                                         (__builtin_bit_cast(uint32_t, Op<QW_DT_BF16>::value(d.w[0] & 0xFFFFu)) & ~f16));
+  } else if (dt == QW_DT_F16) {
+#pragma unroll
+    for (int q = 0; q < V; ++q) v[q] = Op<QW_DT_F16>::value((d.w[q / 2] >> (16 * (q & 1))) & 0xFFFFu);
+  } else {
+#pragma unroll
+    for (int q = 0; q < V; ++q) v[q] = Op<QW_DT_BF16>::value((d.w[q / 2] >> (16 * (q & 1))) & 0xFFFFu);
+  }
 }
 
+template <int DT>
+__device__ inline void store_eight(uint16_t *o, const float (&v)[8]) {
+  u32x4 w;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) w[q] = Op<DT>::bits(v[2 * q]) | (Op<DT>::bits(v[2 * q + 1]) << 16);
+  *reinterpret_cast<u32x4 *>(o) = w;
+}
 // Stores V values at element i, rounded to dt.
 template <int V>
 __device__ inline void store_values(void *p, size_t i, const float (&v)[V], int dt) {
@@ -83,14 +104,12 @@ __device__ inline void store_values(void *p, size_t i, const float (&v)[V], int 
     return;
   }
   uint16_t *o = reinterpret_cast<uint16_t *>(p) + i;
-  if constexpr (V == 8) {
-    u32x4 w;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) w[q] = out_bits(v[2 * q], dt) | (out_bits(v[2 * q + 1], dt) << 16);
-    *reinterpret_cast<u32x4 *>(o) = w;
-  } else {
+  if constexpr (V == 1)
     o[0] = (uint16_t)out_bits(v[0], dt);
-  }
+  else if (dt == QW_DT_F16)
+    store_eight<QW_DT_F16>(o, v);
+  else
+    store_eight<QW_DT_BF16>(o, v);
 }
 
 // V values as bytes of an 8-bit type; they are within its range but for a rounding
@@ -148,7 +167,7 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void norm_kernel(NormArgs a)
   // with perm, the row in its own order: h weight in fp32, or 8-bit elements
   extern __shared__ __attribute__((aligned(16))) float smem[];  // [kRows][K] of either
   __shared__ double sums[W];
-  __shared__ uint32_t tops[W];
+  __shared__ double tops[W];
   const int row_of = W == 1 ? (int)threadIdx.x >> 6 : 0;
   const int m = a.first + (int)blockIdx.x * kRows + row_of;
   if (m >= a.M) return;  // W == 1: whole waves, and no barrier below
@@ -173,32 +192,46 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void norm_kernel(NormArgs a)
     if (w32) {
       Raw<4, V> r;
       load_raw(r, a.weight, k);
-#pragma unroll
-      for (int q = 0; q < V; ++q) g[q] = raw_value(r, q, QW_DT_F32);
+      raw_values(r, g, QW_DT_F32);
     } else {
-#pragma unroll
-      for (int q = 0; q < V; ++q) g[q] = raw_value(gv[i], q, a.w_dtype);
+      raw_values(gv[i], g, a.w_dtype);
     }
   };
   float h[IT][V];
-  float part = 0.0f;
-  uint32_t top = 0;  // the largest |h weight|, as an integer: NaN above infinity above all others
+  // 8 bits: squares and products in 64 bits, so that a row's scale is its formula's,
+  // rounded once (a scale that is off by a step moves all of the row's elements
+  // towards the next borders of the grid)
+  std::conditional_t<IN8, double, float> part = 0;
+  double top = 0.0;         // the largest |h weight|; infinite beside an infinity or a NaN
+  double not_finite = 0.0;  // no number then
 #pragma unroll
   for (int i = 0; i < IT; ++i) {
     const int k = (i * kLanes + at) * V;
     if (k >= K) continue;
+    raw_values(xv[i], h[i], a.x_dtype);
+    if constexpr (RS != 0) {
+      float r[V];
+      raw_values(rv[i], r, a.r_dtype);
+#pragma unroll
+      for (int q = 0; q < V; ++q) h[i][q] += r[q];
+    }
 #pragma unroll
     for (int q = 0; q < V; ++q) {
-      h[i][q] = raw_value(xv[i], q, a.x_dtype);
-      if constexpr (RS != 0) h[i][q] += raw_value(rv[i], q, a.r_dtype);
-      part = __builtin_fmaf(h[i][q], h[i][q], part);
+      if constexpr (IN8)
+        part = __builtin_fma((double)h[i][q], (double)h[i][q], part);
+      else
+        part = __builtin_fmaf(h[i][q], h[i][q], part);
     }
     if (RS != 0 && a.h_out) store_values<V>(a.h_out, row + k, h[i], a.r_dtype);
     float g[V];
     weights(i, k, g);
     if constexpr (IN8) {
 #pragma unroll
-      for (int q = 0; q < V; ++q) top = max(top, __builtin_bit_cast(uint32_t, h[i][q] * g[q]) & 0x7FFFFFFFu);
+      for (int q = 0; q < V; ++q) {
+        const double p = (double)h[i][q] * (double)g[q];
+        top = fmax(top, fabs(p));
+        not_finite += p;
+      }
     } else if constexpr (PERM) {
 #pragma unroll
       for (int q = 0; q < V; ++q) smem[(size_t)row_of * K + k + q] = h[i][q] * g[q];
@@ -207,14 +240,13 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void norm_kernel(NormArgs a)
       for (int q = 0; q < V; ++q) h[i][q] *= g[q];
     }
   }
-  // the lanes' sums are added, and the row's factors computed, in 64 bits: a
-  // common factor that is off moves all elements of an 8-bit row towards the
-  // next borders of the grid (what of it is left is each element's own rounding)
+  // the lanes' sums are added, and the row's factors computed, in 64 bits
   double sum = (double)part;
+  if (IN8 && !(fabs(not_finite) < (double)INFINITY)) top = (double)INFINITY;
 #pragma unroll
   for (int d = 32; d; d >>= 1) {
     sum += __shfl_xor(sum, d, 64);
-    if constexpr (IN8) top = max(top, (uint32_t)__shfl_xor((int)top, d, 64));
+    if constexpr (IN8) top = fmax(top, __shfl_xor(top, d, 64));
   }
   // the row's LDS is written before any of it is read
   auto row_written = [&]() {
@@ -237,7 +269,7 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void norm_kernel(NormArgs a)
 #pragma unroll
     for (int w = 0; w < W; ++w) {
       sum += sums[w];
-      top = max(top, tops[w]);
+      if constexpr (IN8) top = fmax(top, tops[w]);
     }
   } else {
     row_written();
@@ -247,9 +279,9 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void norm_kernel(NormArgs a)
   float f_rest = 0.0f;  // what f's rounding left
   if constexpr (IN8) {
     const double most = a.y_dtype == QW_DT_I8 ? 127.0 : 448.0;
-    const double largest = (double)__builtin_bit_cast(float, top) * inv;
+    const double largest = top * inv;
     // a row with an infinity or a NaN has no scale
-    const bool fine = largest < (double)INFINITY;
+    const bool fine = top <= (double)__FLT_MAX__ && largest < (double)INFINITY;
     const float scale = fine ? fmaxf((float)(largest / most), kLeastScale) : NAN;
     if (at == 0) a.y_scales[m] = scale;
     double factor = fine ? inv / (double)scale : 0.0;

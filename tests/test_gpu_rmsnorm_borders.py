@@ -84,3 +84,21 @@ def test_as_many_rows_as_a_call_takes():
         assert torch.equal(y[at:at + 1], one), at
     at = (1 << 24) - (1 << 19)
     assert bool((y[at:-40] == one).all())
+
+
+@pytest.mark.parametrize("y", ["e4m3", "i8"])
+@pytest.mark.parametrize("x", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("K", [7, 512, 2048, 5120, 8192, 16384, 32768])
+def test_scales_are_the_formulas_rounded_once(K, x, y):
+    """A row's scale is off by half a step of fp32 and some 64-bit roundings, an element
+    nearest to its number but for two roundings of it (the factor's and its own);
+    rows of 1e25, whose squares fp32 cannot hold, too."""
+    X, _, W, P = inputs(200, K, x, None, K + 2, "f32")
+    if x != "f16":
+        X[::50] = X[::50] * 1e25
+    want = formula(X, None, W, 1e-6)[1]
+    for perm in (None, P):
+        n = qw.qw_rmsnorm(X.cuda(), W.cuda(), perm=None if perm is None else perm.cuda(), out_dtype=xdt(y))
+        s = np.abs(want).max(1) / TOP[y]
+        assert (np.abs(n.scales.double().cpu().numpy() - s) <= F32 * (1 + 2.0 ** -20) * s).all()
+        nearest(n, want if perm is None else want[:, perm.numpy()], y, 2 * F32)
