@@ -505,10 +505,9 @@ __device__ inline void choose_tokens(const ScoredArgs &a, int t0, int count, int
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
     __builtin_amdgcn_wave_barrier();
     int id = sub < a.k ? chosen[sub] : -1;
-    float l = id >= 0 ? logit_at<DT>(a.logits, (size_t)t * a.E + id) : 0.0f;
     if (!a.bias) {  // a choice and the next, or the last and the first that is none, may have one score
       const int lane = threadIdx.x & 63;
-      const bool level = id >= 0 && may_level(a, l, most);
+      const bool level = id >= 0 && may_level(a, logit_at<DT>(a.logits, (size_t)t * a.E + id), most);
       const unsigned long long others = __ballot(id >= 0 && !level);
       if (level && (sub == a.k - 1 || !((others >> ((lane + 1) & 63)) & 1))) sure = false;
     }
@@ -519,12 +518,11 @@ __device__ inline void choose_tokens(const ScoredArgs &a, int t0, int count, int
       if ((doubts >> ((threadIdx.x & 63) / L * L)) & kToken) {
         id = id64;
         if (sub < a.k) chosen[sub] = id;
-        l = id >= 0 ? logit_at<DT>(a.logits, (size_t)t * a.E + id) : 0.0f;
       }
     }
     // normalised weights do not need the sum over all experts
     const double sum = softmax && !a.normalize ? sum64<L>(x, most) : 1.0;
-    const double w = id >= 0 ? score64(a, l, most, sum) : 0.0;
+    const double w = id >= 0 ? score64(a, logit_at<DT>(a.logits, (size_t)t * a.E + id), most, sum) : 0.0;
     double factor = (double)a.scale;
     if (a.normalize) {
       const double total = sum_of<L>(w);
