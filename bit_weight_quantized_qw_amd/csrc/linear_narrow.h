@@ -11,8 +11,10 @@
 //
 // Measured, 7 rows of 8192 x 28672: INT4 with anchors and e4m3 rows 42 us (3.2
 // TB/s), NF4 41, 2-bit with anchors 59; one row in NF4 33. What bounds them: the
-// loads' address units, busy 0.60 of the cycles in the first of these (a load
-// touches 16 rows), beside 0.38 of vector issue and 0.09 of matrix products.
+// loads' address units, busy 0.58 of the cycles in the first of these, beside 0.38
+// of vector issue and 0.09 of matrix products. A load touches 16 rows because a lane
+// takes the column whose operand it holds; consecutive bytes of one row by a run of
+// lanes, turned in LDS, would touch fewer, and have not been tried here.
 #pragma once
 
 #include "linear.h"

@@ -16,8 +16,8 @@
 // turns the row: h weight in fp32, or the 8-bit elements as they are.
 //
 // Measured: 8192 x 8192 in bf16 with the residual, y in bf16 96 us (5.6 TB/s; a
-// copy of 1 GiB here 5.2), in e4m3 89, permuted 102 (8 K single bytes a row from
-// LDS); 8192 x 1024 11.6 us (5.8 TB/s); 777 x 5120 with an fp32 residual 10.2 us, in
+// copy of 1 GiB here 5.2), in e4m3 89, permuted 102 (each
+// byte by a read of LDS of its own); 8192 x 1024 11.6 us (5.8 TB/s); 777 x 5120 with an fp32 residual 10.2 us, in
 // a permuted order 11.8; one row of 5120 4.2 us. Rows that do not start on 16 bytes
 // (K not a multiple of 8) go by single elements: 4096 x 5119 70 us, 2.4 TB/s.
 #include <math.h>

@@ -774,8 +774,9 @@ qw_status qw_lora_add(const qw_adapters *ad, const void *x, const qw_groups *g,
  *                the scale NaN and zeros.
  * A row is read whole before any of it is written: residual_out may be
  * residual, and y may be x, if their types have one size and no other buffer
- * overlaps. Sums are fp32 (a row of values beyond 2^60 overflows them), y is
- * rounded once. eps is finite and >= 0 (a zero row at eps = 0 is NaN).
+ * overlaps. h is fp32. Sums are fp32 for y in 16 and 32 bits (a row of values
+ * beyond 2^60 overflows them, one below 2^-60 underflows, which shows where eps is
+ * as small), 64 bits for y in 8; y is rounded once. eps is finite and >= 0 (a zero row at eps = 0 is NaN).
  * Errors: INVALID_ARG (also residual_out without residual, y_scales given or
  * missing against y_dtype), ALIGNMENT, UNSUPPORTED (K > QW_MAX_NORM_K,
  * M > QW_MAX_ROWS), HIP. */
